@@ -23,7 +23,7 @@ EXPORTS = ("attn_fwd", "attn_fwd_ex", "attn_status_string", "attn_debug_error", 
            "attn_bwd", "attn_bwd_ex", "attn_bwd_workspace_bytes", "attn_bwd_debug_error",
            "attn_decode", "attn_decode_ex", "attn_decode_workspace_bytes", "attn_decode_num_splits",
            "attn_decode_debug_error", "attn_fwd_fp8", "attn_fwd_fp8_ex", "attn_merge", "attn_fwd_host",
-           "attn_fwd_fp8_host", "attn_decode_static")
+           "attn_fwd_fp8_host", "attn_decode_static", "attn_kv_append", "attn_kv_append_debug_error")
 
 _lib = None
 
@@ -39,6 +39,16 @@ class FwdOptions(ctypes.Structure):
     _fields_ = [("wait_timeout_ns", ctypes.c_uint64), ("inject_stall", ctypes.c_int),
                 ("grid_ctas", ctypes.c_int), ("item_visits", ctypes.c_void_p), ("p_bf16", ctypes.c_int),
                 ("out_fp32", ctypes.c_int), ("key_offset", ctypes.c_int64), ("bwd_deterministic", ctypes.c_int)]
+
+
+class KvAppendArgs(ctypes.Structure):
+    """attn_kv_append_args of include/attn.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")] + \
+               [(n, ctypes.c_void_p) for n in ("q_out", "k_cache", "v_cache", "k_scale", "v_scale", "block_table",
+                                               "seq_lens", "cu_tokens", "positions", "inv_freq")] + \
+               [(n, ctypes.c_int64) for n in ("B", "T", "Hq", "Hkv", "d", "rot_dim", "num_pages", "page_size",
+                                              "max_pages_per_seq", "scale_block")] + [("interleaved", ctypes.c_int)]
 
 
 def lib_path() -> str:
@@ -99,6 +109,10 @@ def load_library():
     lib.attn_fwd_host.restype = ctypes.c_int
     lib.attn_fwd_fp8_host.argtypes = [vp, vp, vp, f32, f32, f32] + host_tail
     lib.attn_fwd_fp8_host.restype = ctypes.c_int
+    lib.attn_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), vp]
+    lib.attn_kv_append.restype = ctypes.c_int
+    lib.attn_kv_append_debug_error.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
+    lib.attn_kv_append_debug_error.restype = ctypes.c_int
     lib.attn_merge.argtypes = [vp, vp, vp, vp, vp, i64, i64, ctypes.c_int, vp]
     lib.attn_merge.restype = ctypes.c_int
     _lib = lib
@@ -398,6 +412,123 @@ def decode_static(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if st != 0:
         raise AttnError(st, "attn_decode_static")
     return out, lse
+
+
+def _rows(t: torch.Tensor, name: str, T, H, d):
+    """Token rows [T, H, d] in bf16, each row contiguous, any distance from row to row."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA torch.bfloat16 tensor with 3 dims")
+    shape, (s0, s1, s2) = t.shape, t.stride()
+    if (T is not None and shape[0] != T) or (H is not None and shape[1] != H) or (d is not None and shape[2] != d):
+        raise ValueError(f"{name} has the wrong shape")
+    if (s2 != 1 and shape[2] > 1) or (s1 != shape[2] and shape[1] > 1):
+        raise ValueError(f"each row of {name} must be contiguous")
+    return s0 if shape[0] > 1 else max(s0, shape[1] * shape[2])
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              block_table: torch.Tensor, seq_lens: torch.Tensor, q: Optional[torch.Tensor] = None,
+              cu_tokens: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+              inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False,
+              k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+              q_out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+              ) -> Optional[torch.Tensor]:
+    """Append new tokens to a paged KV cache, rotating keys (and queries) by their positions.
+
+    k, v: [T, Hkv, d] bf16, token rows sequence after sequence (rows may be views of one
+    projection's output); k_cache/v_cache: [num_pages, Hkv, page_size, d], bf16, or E4M3
+    codes (uint8 or float8_e4m3fn) with ``k_scale``/``v_scale`` fp32
+    [num_pages, Hkv, page_size / block]; block_table [B, max_pages] and seq_lens [B] int32 as
+    in ``decode`` (new tokens included).  ``cu_tokens`` (int32 [B + 1]) gives each sequence's
+    rows; without it every sequence has T / B.  ``inv_freq`` (fp32 [rot / 2]) turns the
+    rotation on, by the cache's positions or ``positions`` (int32 [T]).  With ``q``
+    [T, Hq, d] its rotated rows are returned: [B, Hq, T / B, d] as ``decode`` takes them, or
+    [T, Hq, d] with ``cu_tokens``.  One launch on ``stream`` (default: the current stream).
+    """
+    lib = load_library()
+    k_stride = _rows(k, "k", None, None, None)
+    T, Hkv, d = k.shape
+    v_stride = _rows(v, "v", T, Hkv, d)
+    fp8 = k_scale is not None or v_scale is not None
+    if fp8:
+        k_cache, v_cache = _codes(k_cache, "k_cache"), _codes(v_cache, "v_cache")
+        _check(k_scale, "k_scale", torch.float32, 3)
+        _check(v_scale, "v_scale", torch.float32, 3)
+    else:
+        _check(k_cache, "k_cache", torch.bfloat16, 4)
+        _check(v_cache, "v_cache", torch.bfloat16, 4)
+    _check(block_table, "block_table", torch.int32, 2)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    num_pages, heads, page_size, dk = k_cache.shape
+    B, max_pages = block_table.shape
+    if (heads, dk) != (Hkv, d) or v_cache.shape != k_cache.shape or seq_lens.shape[0] != B:
+        raise ValueError("k, cache, block_table and seq_lens shapes disagree")
+    block = 0
+    if fp8:
+        per_page = k_scale.shape[2]
+        if k_scale.shape != v_scale.shape or tuple(k_scale.shape[:2]) != (num_pages, Hkv) or per_page < 1 \
+                or page_size % per_page:
+            raise ValueError("k_scale and v_scale must be [num_pages, Hkv, page_size / block]")
+        block = page_size // per_page
+    a = KvAppendArgs(k=k.data_ptr(), v=v.data_ptr(), k_stride=k_stride, v_stride=v_stride,
+                     k_cache=k_cache.data_ptr(), v_cache=v_cache.data_ptr(), block_table=block_table.data_ptr(),
+                     seq_lens=seq_lens.data_ptr(), B=B, T=T, Hkv=Hkv, d=d, num_pages=num_pages, page_size=page_size,
+                     max_pages_per_seq=max_pages, scale_block=block, interleaved=1 if interleaved else 0)
+    given = [v, k_cache, v_cache, block_table, seq_lens]
+    if fp8:
+        a.k_scale, a.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+        given += [k_scale, v_scale]
+    for t, name, dtype in ((cu_tokens, "cu_tokens", torch.int32), (positions, "positions", torch.int32),
+                           (inv_freq, "inv_freq", torch.float32)):
+        if t is not None:
+            _check(t, name, dtype, 1)
+            setattr(a, name, t.data_ptr())
+            given.append(t)
+    if cu_tokens is not None and cu_tokens.shape[0] != B + 1:
+        raise ValueError("cu_tokens must have B + 1 entries")
+    if cu_tokens is None and (B < 1 or T % B):
+        raise ValueError("without cu_tokens the number of tokens must be a multiple of the number of sequences")
+    if positions is not None and positions.shape[0] != T:
+        raise ValueError("positions must have one entry for each token")
+    if inv_freq is not None:
+        a.rot_dim = 2 * inv_freq.shape[0]
+    if q is not None:
+        a.q_stride = _rows(q, "q", T, None, d)
+        a.q, a.Hq = q.data_ptr(), q.shape[1]
+        given.append(q)
+        shape = (T, q.shape[1], d) if cu_tokens is not None else (B, q.shape[1], T // B, d)
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        _check(q_out, "q_out", torch.bfloat16, len(shape))
+        if tuple(q_out.shape) != shape:
+            raise ValueError("q_out has the wrong shape")
+        given.append(q_out)
+        a.q_out = q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    device = k.device
+    if any(t.device != device for t in given):
+        raise ValueError("all tensors must be on one device")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    with torch.cuda.device(device):
+        st = lib.attn_kv_append(ctypes.byref(a), ctypes.c_void_p(stream.cuda_stream))
+    if st != 0:
+        raise AttnError(st, "attn_kv_append")
+    return q_out
+
+
+def kv_append_debug_error(stream: Optional[torch.cuda.Stream] = None, device=None) -> Tuple[int, int]:
+    """Synchronise and read/clear the append's error word: (status, raw code)."""
+    lib = load_library()
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    code = ctypes.c_int(0)
+    with torch.cuda.device(stream.device):
+        st = lib.attn_kv_append_debug_error(ctypes.c_void_p(stream.cuda_stream), ctypes.byref(code))
+    return st, code.value
 
 
 def merge(acc_out: torch.Tensor, acc_lse: torch.Tensor, part_out: torch.Tensor, part_lse: torch.Tensor,

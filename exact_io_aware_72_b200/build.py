@@ -10,7 +10,7 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libattn_b200.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("attn_fwd.cu", "attn_bwd.cu", "attn_decode.cu", "attn_merge.cu",
-                                                "attn_fwd_host.cu")]
+                                                "attn_fwd_host.cu", "attn_append.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("attn_fwd_kernel.cuh", "attn_bwd_kernel.cuh", "attn_decode_kernel.cuh", "sm100_ptx.cuh")] + [
     os.path.join(ROOT, "include", "attn.h")]
 
@@ -23,7 +23,7 @@ def nvcc_path() -> str:
 
 
 def nvcc_command(out: str = LIB_PATH, extra=()) -> list:
-    return [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
+    return [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17", "--threads", "0",
             "-Xcompiler", "-fPIC", "-shared", "-I" + os.path.join(ROOT, "include"), *extra,
             "-o", out, *SOURCES]
 

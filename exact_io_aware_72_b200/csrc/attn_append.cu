@@ -1,0 +1,548 @@
+// The write side of the paged KV cache declared in include/attn.h: new tokens' keys and
+// values go into their sequences' pages, the keys (and the queries of the same tokens)
+// rotated by their positions on the way; the cache holds bf16 values or E4M3 codes with a
+// power-of-two scale for each block of tokens and head.
+//
+// Rotation of a pair (a, b) at position x with frequency f: (a c - b s, b c + a s) with
+// c = cos(x f), s = sin(x f).  An angle of a far position (2^17 and more) needs more bits
+// than fp32 has: x f is formed in fp64 as turns, x f / 2 pi, whose distance from the
+// nearest whole turn (at most a half) goes to fp32, so cos and sin are good to about one
+// fp32 rounding at every position.  The rotation itself is fp32, rounded once (to bf16, or
+// to the E4M3 code).
+//
+// Scales are powers of two (the smallest s >= 2^-40 with amax <= 448 s): E4M3 is a floating
+// format, so a finer scale would only shift its exponent window, while with powers of two
+// the division x / s is exact and raising a block's scale only moves its older codes'
+// exponents (a code is rounded again only where it turns subnormal).
+//
+// What bounds it: HBM for prefill chunks (every row is read once and written once), the
+// latency of the chain length -> page -> store for a decoding step's few rows.  One CTA
+// takes one unit: the new tokens of one sequence that fall into one aligned run of `unit`
+// slots (a block, or 16 slots), so a block's largest magnitude is found inside one CTA, in
+// a fixed order, without atomics.  The unit's cos / sin table is computed once into shared
+// memory and used by all of the CTA's heads; the heads are dealt over gridDim.y when there
+// are few units.
+#include "attn.h"
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include "sm100_ptx.cuh"
+
+namespace attn_sm100_app {
+using namespace attn_sm100;
+
+constexpr int kAppThreads = 256;
+constexpr int kErrSeq = 1 << 20;   // a sequence's length or token range is unusable
+constexpr int kErrPage = 2 << 20;  // a page-table entry the call needs is out of range
+
+// Device error word (read and cleared by attn_kv_append_debug_error).
+__device__ int g_attn_app_error;
+
+struct AppParams {
+  const __nv_bfloat16 *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;  // elements from token to token
+  __nv_bfloat16* q_out;
+  void *k_cache, *v_cache;               // bf16 values or E4M3 codes
+  float *k_scale, *v_scale;
+  const int *block_table, *seq_lens, *cu_tokens, *positions;
+  const float* inv_freq;
+  int* err;
+  int64_t T;
+  int B, Hq, Hkv, half;                  // half = rotated pairs
+  int interleaved;
+  int page_size, num_pages, max_pages;
+  int unit;                              // slots of a unit (a multiple of block)
+  int block;                             // slots that share a scale
+  int per_seq;                           // equal sequences: tokens of each (0: cu_tokens)
+  int units_per_seq;                     // equal sequences: upper bound
+};
+
+struct Unit {
+  int b;
+  int t0, n;     // first token row of the unit, number of new tokens in it
+  int slot0;     // slot of the first new token inside the unit
+  int pos0;      // position of the first new token
+  int64_t page;  // physical page, -1 if unusable
+  int in_page;   // first slot of the unit inside its page
+  int first;     // the sequence's first token row
+};
+
+// Which tokens CTA `idx` takes.  Called by one whole warp; n = 0 when there are none.
+__device__ __forceinline__ Unit find_unit(const AppParams& p, int idx, int lane) {
+  Unit u{0, 0, 0, 0, 0, -1, 0, 0};
+  int len = 0, n = 0, first = 0, j = 0;
+  if (p.per_seq) {
+    u.b = idx / p.units_per_seq;
+    j = idx - u.b * p.units_per_seq;
+    n = p.per_seq;
+    first = u.b * n;
+    len = __ldg(p.seq_lens + u.b);
+    if (len < n || len > p.max_pages * p.page_size) {
+      if (lane == 0) atomicCAS(p.err, 0, kErrSeq | (u.b & 0xFFFFF));
+      return u;
+    }
+    if (j > (len - 1) / p.unit - (len - n) / p.unit) return u;
+  } else {
+    // Units are numbered sequence by sequence: a running count over 32 sequences at a time.
+    int before = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < p.B && !found; b0 += 32) {
+      const int b = b0 + lane;
+      int l = 0, c0 = 0, m = 0, cnt = 0;
+      if (b < p.B) {
+        c0 = __ldg(p.cu_tokens + b);
+        const int c1 = __ldg(p.cu_tokens + b + 1);
+        l = __ldg(p.seq_lens + b);
+        m = c1 - c0;
+        if (c0 < 0 || m < 0 || c1 > p.T || (m > 0 && (l < m || l > p.max_pages * p.page_size))) {
+          atomicCAS(p.err, 0, kErrSeq | (b & 0xFFFFF));
+        } else if (m > 0) {
+          cnt = (l - 1) / p.unit - (l - m) / p.unit + 1;
+        }
+      }
+      int incl = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const unsigned here = __ballot_sync(0xffffffffu, before + incl > idx);
+      if (here) {
+        const int at = __ffs(here) - 1;
+        u.b = b0 + at;
+        len = __shfl_sync(0xffffffffu, l, at);
+        n = __shfl_sync(0xffffffffu, m, at);
+        first = __shfl_sync(0xffffffffu, c0, at);
+        j = idx - before - __shfl_sync(0xffffffffu, incl - cnt, at);
+        found = true;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (!found) return u;
+  }
+  const int p0 = len - n;                            // position of the sequence's first new token
+  const int run = (p0 / p.unit + j) * p.unit;        // first position of the unit
+  u.pos0 = max(run, p0);
+  u.n = min(run + p.unit, len) - u.pos0;
+  u.slot0 = u.pos0 - run;
+  u.first = first;
+  u.t0 = first + (u.pos0 - p0);
+  u.in_page = run % p.page_size;
+  const int entry = __ldg(p.block_table + static_cast<int64_t>(u.b) * p.max_pages + run / p.page_size);
+  if (entry >= 0 && entry < p.num_pages) {
+    u.page = entry;
+  } else if (lane == 0) {
+    atomicCAS(p.err, 0, kErrPage | (u.b & 0xFFFFF));
+  }
+  return u;
+}
+
+__device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
+  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(r[i] << 16);
+    x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
+  return make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
+}
+
+// Element offsets of the two 8-element chunks of lane c of a row (D / 16 lanes): chunk
+// pairs (8c, half + 8c) in the rotated part of the half-split form; elsewhere, and in the
+// interleaved form, 16 consecutive elements.
+__device__ __forceinline__ void chunk_at(const AppParams& p, int c, int& lo, int& hi) {
+  if (!p.interleaved && 8 * c < p.half) {
+    lo = 8 * c;
+    hi = p.half + 8 * c;
+  } else {
+    lo = 16 * c;
+    hi = 16 * c + 8;
+  }
+}
+
+// Rotates a lane's 16 elements in place; cs = the token's (cos, sin) of pairs 8c .. 8c + 7.
+__device__ __forceinline__ void rotate16(bool interleaved, const float2* cs, float (&a)[8], float (&b)[8]) {
+  if (!interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = a[i], y = b[i];
+      a[i] = x * cs[i].x - y * cs[i].y;
+      b[i] = y * cs[i].x + x * cs[i].y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float x = a[i], y = a[i + 1], z = b[i], w = b[i + 1];
+      const float2 c0 = cs[i / 2], c1 = cs[4 + i / 2];
+      a[i] = x * c0.x - y * c0.y;
+      a[i + 1] = y * c0.x + x * c0.y;
+      b[i] = z * c1.x - w * c1.y;
+      b[i + 1] = w * c1.x + z * c1.y;
+    }
+  }
+}
+
+// The smallest power of two s >= 2^-40 with amax <= 448 s (amax finite): 448 = 1.75 * 2^8.
+__device__ __forceinline__ float block_scale(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int e = static_cast<int>(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
+  return __uint_as_float(static_cast<uint32_t>(max(e, -40) + 127) << 23);
+}
+__device__ __forceinline__ float finite_mag(float x) {
+  const float m = fabsf(x);
+  return m <= 3.402823466e38f ? m : 0.f;  // NaN and infinities do not set a scale
+}
+// Eight values to E4M3 codes of x / s.
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float s, float inv, bool pow2) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = pow2 ? x[i] * inv : __fdiv_rn(x[i], s);
+  return make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
+}
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(code & 0xffu));
+  float f;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h));
+  return f;
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_constant__ AppParams p) {
+  constexpr int G = D / 16;                  // lanes of a row
+  constexpr int kRows = kAppThreads / G;     // rows a pass of the CTA takes
+  extern __shared__ float2 s_cs[];           // [unit][half] (cos, sin) of the unit's tokens
+  __shared__ Unit s_unit;
+  __shared__ float s_amax[2][kAppThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < 32) {
+    const Unit u = find_unit(p, blockIdx.x, lane);
+    if (lane == 0) s_unit = u;
+  }
+  __syncthreads();
+  const Unit u = s_unit;
+  if (u.n == 0) return;
+  for (int i = tid; i < u.n * p.half; i += kAppThreads) {
+    const int t = i / p.half, f = i - t * p.half;
+    const int pos = p.positions ? __ldg(p.positions + u.t0 + t) : u.pos0 + t;
+    const double turns = static_cast<double>(pos) * static_cast<double>(__ldg(p.inv_freq + f)) * 0.15915494309189535;
+    const float r = static_cast<float>(turns - rint(turns));
+    float sn, cn;
+    sincospif(2.f * r, &sn, &cn);
+    s_cs[i] = make_float2(cn, sn);
+  }
+  __syncthreads();
+  const int c = tid % G, g = tid / G;
+  int at_lo, at_hi;
+  chunk_at(p, c, at_lo, at_hi);
+  const bool turn = 8 * c < p.half;
+  const int parts = gridDim.y, part = blockIdx.y;
+
+  // Queries: rotated into the decoding step's layout [B, Hq, Nq, d] (equal sequences) or
+  // left token-major.
+  if (p.q) {
+    const int h0 = static_cast<int>(static_cast<int64_t>(p.Hq) * part / parts);
+    const int h1 = static_cast<int>(static_cast<int64_t>(p.Hq) * (part + 1) / parts);
+    const int rows = u.n * (h1 - h0);
+    for (int r = g; r < rows; r += kRows) {
+      const int t = r / (h1 - h0), h = h0 + r - t * (h1 - h0);
+      const __nv_bfloat16* src = p.q + (u.t0 + t) * p.q_stride + h * D;
+      float a[8], b[8];
+      widen8(__ldg(reinterpret_cast<const uint4*>(src + at_lo)), a);
+      widen8(__ldg(reinterpret_cast<const uint4*>(src + at_hi)), b);
+      if (turn) rotate16(p.interleaved, s_cs + t * p.half + 8 * c, a, b);
+      const int64_t row = p.per_seq
+                              ? (static_cast<int64_t>(u.b) * p.Hq + h) * p.per_seq + (u.t0 + t - u.first)
+                              : static_cast<int64_t>(u.t0 + t) * p.Hq + h;
+      __nv_bfloat16* dst = p.q_out + row * D;
+      *reinterpret_cast<uint4*>(dst + at_lo) = narrow8(a);
+      *reinterpret_cast<uint4*>(dst + at_hi) = narrow8(b);
+    }
+  }
+  if (u.page < 0) return;
+  const int h0 = static_cast<int>(static_cast<int64_t>(p.Hkv) * part / parts);
+  const int h1 = static_cast<int>(static_cast<int64_t>(p.Hkv) * (part + 1) / parts);
+  if constexpr (!FP8) {
+    const int rows = u.n * (h1 - h0) * 2;
+    for (int r = g; r < rows; r += kRows) {
+      const int kv = r & 1, i = r >> 1;
+      const int t = i / (h1 - h0), h = h0 + i - t * (h1 - h0);
+      const __nv_bfloat16* src = (kv ? p.v + (u.t0 + t) * p.v_stride : p.k + (u.t0 + t) * p.k_stride) + h * D;
+      uint4 lo = __ldg(reinterpret_cast<const uint4*>(src + at_lo));
+      uint4 hi = __ldg(reinterpret_cast<const uint4*>(src + at_hi));
+      if (!kv && turn) {
+        float a[8], b[8];
+        widen8(lo, a);
+        widen8(hi, b);
+        rotate16(p.interleaved, s_cs + t * p.half + 8 * c, a, b);
+        lo = narrow8(a);
+        hi = narrow8(b);
+      }
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(kv ? p.v_cache : p.k_cache) +
+                           ((u.page * p.Hkv + h) * p.page_size + u.in_page + u.slot0 + t) * D;
+      *reinterpret_cast<uint4*>(dst + at_lo) = lo;
+      *reinterpret_cast<uint4*>(dst + at_hi) = hi;
+    }
+  } else {
+    // The unit's blocks one after another; in a block, half of the CTA takes K and half V.
+    constexpr int kPass = kRows / 2;
+    const int kv = g / kPass, r0 = g - kv * kPass;
+    const __nv_bfloat16* base = kv ? p.v : p.k;
+    const int64_t stride = kv ? p.v_stride : p.k_stride;
+    uint8_t* cache = static_cast<uint8_t*>(kv ? p.v_cache : p.k_cache);
+    float* scales = kv ? p.v_scale : p.k_scale;
+    const int blocks_per_page = p.page_size / p.block;
+    auto load = [&](int t, int h, float (&a)[8], float (&b)[8]) {
+      const __nv_bfloat16* src = base + (u.t0 + t) * stride + h * D;
+      widen8(__ldg(reinterpret_cast<const uint4*>(src + at_lo)), a);
+      widen8(__ldg(reinterpret_cast<const uint4*>(src + at_hi)), b);
+      if (!kv && turn) rotate16(p.interleaved, s_cs + t * p.half + 8 * c, a, b);
+    };
+    for (int h = h0; h < h1; ++h) {
+      for (int s0 = u.slot0 / p.block * p.block; s0 < u.slot0 + u.n; s0 += p.block) {
+        const int ta = max(s0 - u.slot0, 0), tb = min(s0 + p.block - u.slot0, u.n);  // its new tokens [ta, tb)
+        const int held = max(u.slot0 - s0, 0);                                      // slots filled before
+        float amax = 0.f;
+        for (int t = ta + r0; t < tb; t += kPass) {
+          float a[8], b[8];
+          load(t, h, a, b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(finite_mag(a[i]), finite_mag(b[i])));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        __syncthreads();  // the previous block's maxima have been read
+        if (lane == 0) s_amax[kv][tid / 32] = amax;
+        __syncthreads();
+        constexpr int kHalfWarps = kAppThreads / 64;
+        amax = 0.f;
+#pragma unroll
+        for (int w = 0; w < kHalfWarps; ++w) amax = fmaxf(amax, s_amax[kv][kv * kHalfWarps + w]);
+        const int64_t head = u.page * p.Hkv + h;
+        float* sc = scales + head * blocks_per_page + (u.in_page + s0) / p.block;
+        const float old = held ? *sc : 0.f;
+        const bool keep = held && old >= 1.17549435e-38f && amax <= 448.f * old;
+        const float s = keep ? old : block_scale(amax);
+        uint8_t* rows = cache + (head * p.page_size + u.in_page) * D;
+        const float inv = 1.f / s;
+        const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
+        for (int t = ta + r0; t < tb; t += kPass) {
+          float a[8], b[8];
+          load(t, h, a, b);
+          uint8_t* dst = rows + (u.slot0 + t) * D;
+          *reinterpret_cast<uint2*>(dst + at_lo) = encode8(a, s, inv, pow2);
+          *reinterpret_cast<uint2*>(dst + at_hi) = encode8(b, s, inv, pow2);
+        }
+        if (held && !keep) {
+          // Codes that were here before, under the new scale.
+          const float ratio = old / s;
+          for (int r = r0; r < held; r += kPass) {
+            uint4* at = reinterpret_cast<uint4*>(rows + (s0 + r) * D + 16 * c);
+            const uint4 w = *at;
+            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            uint32_t out[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              out[i] = pack_e4m3x4(e4m3_value(in[i]) * ratio, e4m3_value(in[i] >> 8) * ratio,
+                                   e4m3_value(in[i] >> 16) * ratio, e4m3_value(in[i] >> 24) * ratio);
+            *at = make_uint4(out[0], out[1], out[2], out[3]);
+          }
+        }
+        if (held) __syncthreads();  // every thread has read the old scale
+        if (!keep && r0 == 0 && c == 0) *sc = s;
+      }
+    }
+  }
+}
+
+}  // namespace attn_sm100_app
+
+using namespace attn_sm100_app;
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+struct AppDevice {
+  bool probed = false;
+  bool supported = false;
+  int sm_count = 0;
+  int* err_word = nullptr;
+};
+std::mutex g_app_mutex;
+AppDevice g_app_dev[kMaxDevices];
+
+template <int D, bool FP8>
+bool allow_smem(int bytes) {
+  return cudaFuncSetAttribute(attn_append_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+         cudaSuccess;
+}
+
+int app_device_setup(AppDevice& out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lock(g_app_mutex);
+  AppDevice& info = g_app_dev[dev];
+  if (!info.probed) {
+    int major = 0, minor = 0, sms = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+    info.supported = (major == 10 && minor == 0);
+    info.sm_count = sms;
+    if (info.supported) {
+      void* addr = nullptr;
+      if (cudaGetSymbolAddress(&addr, g_attn_app_error) != cudaSuccess) return ATTN_ERR_CUDA;
+      info.err_word = static_cast<int*>(addr);
+      // a unit of 256 slots: 256 x d/2 pairs of 8 bytes
+      if (!allow_smem<64, true>(256 * 32 * 8) || !allow_smem<128, true>(256 * 64 * 8)) return ATTN_ERR_CUDA;
+    }
+    info.probed = true;
+  }
+  out = info;
+  return info.supported ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
+
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b || na == 0 || nb == 0) return false;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  return pa < pb + nb && pb < pa + na;
+}
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+
+extern "C" int attn_kv_append(const attn_kv_append_args* a, cudaStream_t stream) {
+  if (!a) return ATTN_ERR_INVALID_ARG;
+  const bool fp8 = a->scale_block != 0;
+  if ((a->T > 0 && (!a->k || !a->v)) || !a->k_cache || !a->v_cache || !a->block_table || !a->seq_lens)
+    return ATTN_ERR_INVALID_ARG;
+  if (fp8 != (a->k_scale != nullptr) || fp8 != (a->v_scale != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (a->T > 0 && (a->q != nullptr) != (a->q_out != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (a->B < 1 || a->T < 0 || a->Hkv < 1 || (a->q && a->Hq < 1) || a->num_pages < 1 || a->max_pages_per_seq < 1)
+    return ATTN_ERR_INVALID_ARG;
+  if (!a->cu_tokens && a->T % a->B != 0) return ATTN_ERR_INVALID_ARG;
+  if (a->d != 64 && a->d != 128) return ATTN_ERR_UNSUPPORTED;
+  const int64_t ps = a->page_size;
+  if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256) return ATTN_ERR_UNSUPPORTED;
+  if (a->rot_dim < 0 || a->rot_dim > a->d || (a->rot_dim > 0) != (a->inv_freq != nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (a->rot_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+  if (fp8 && (a->scale_block < 1 || a->scale_block > ps || (a->scale_block & (a->scale_block - 1)) != 0))
+    return ATTN_ERR_INVALID_ARG;
+  const int64_t Hq = a->q ? a->Hq : 0, lim = 0x7fffffff;
+  if (a->T > lim || a->B > (int64_t(1) << 30) || Hq > (int64_t(1) << 20) || a->Hkv > (int64_t(1) << 20) ||
+      a->num_pages > lim / a->Hkv || a->max_pages_per_seq > lim / ps || a->B > lim / a->max_pages_per_seq)
+    return ATTN_ERR_INVALID_ARG;
+  if (a->k_stride < a->Hkv * a->d || a->v_stride < a->Hkv * a->d || (a->q && a->q_stride < Hq * a->d) ||
+      a->k_stride > (int64_t(1) << 31) || a->v_stride > (int64_t(1) << 31) ||
+      (a->q && a->q_stride > (int64_t(1) << 31)))
+    return ATTN_ERR_INVALID_ARG;
+  if (a->k_stride % 8 != 0 || a->v_stride % 8 != 0 || (a->q && a->q_stride % 8 != 0)) return ATTN_ERR_MISALIGNED;
+  if (!aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->q, 16) || !aligned(a->q_out, 16) ||
+      !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) || !aligned(a->k_scale, 4) || !aligned(a->v_scale, 4) ||
+      !aligned(a->block_table, 4) || !aligned(a->seq_lens, 4) || !aligned(a->cu_tokens, 4) ||
+      !aligned(a->positions, 4) || !aligned(a->inv_freq, 4))
+    return ATTN_ERR_MISALIGNED;
+  // Everything written must lie apart from everything else.
+  const size_t cache = static_cast<size_t>(a->num_pages) * a->Hkv * ps * a->d * (fp8 ? 1 : 2);
+  const size_t scale = fp8 ? static_cast<size_t>(a->num_pages) * a->Hkv * (ps / a->scale_block) * 4 : 0;
+  auto span = [&](int64_t stride, int64_t heads) -> size_t {
+    return a->T ? static_cast<size_t>((a->T - 1) * stride + heads * a->d) * 2 : 0;
+  };
+  const void* outs[5] = {a->k_cache, a->v_cache, a->k_scale, a->v_scale, a->q_out};
+  const size_t out_sz[5] = {cache, cache, scale, scale, static_cast<size_t>(a->T) * Hq * a->d * 2};
+  const void* ins[8] = {a->k, a->v, a->q, a->block_table, a->seq_lens, a->cu_tokens, a->positions, a->inv_freq};
+  const size_t in_sz[8] = {span(a->k_stride, a->Hkv), span(a->v_stride, a->Hkv), a->q ? span(a->q_stride, Hq) : 0,
+                           static_cast<size_t>(a->B) * a->max_pages_per_seq * 4, static_cast<size_t>(a->B) * 4,
+                           static_cast<size_t>(a->B + 1) * 4, static_cast<size_t>(a->T) * 4,
+                           static_cast<size_t>(a->rot_dim) * 2};
+  for (int o = 0; o < 5; ++o) {
+    for (int i = 0; i < 8; ++i)
+      if (overlaps(outs[o], out_sz[o], ins[i], in_sz[i])) return ATTN_ERR_INVALID_ARG;
+    for (int o2 = o + 1; o2 < 5; ++o2)
+      if (overlaps(outs[o], out_sz[o], outs[o2], out_sz[o2])) return ATTN_ERR_INVALID_ARG;
+  }
+
+  AppDevice dev;
+  const int st = app_device_setup(dev);
+  if (st != ATTN_OK) return st;
+  if (a->T == 0) return ATTN_OK;
+
+  AppParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(a->q);
+  p.k = static_cast<const __nv_bfloat16*>(a->k);
+  p.v = static_cast<const __nv_bfloat16*>(a->v);
+  p.q_stride = a->q_stride;
+  p.k_stride = a->k_stride;
+  p.v_stride = a->v_stride;
+  p.q_out = static_cast<__nv_bfloat16*>(a->q_out);
+  p.k_cache = a->k_cache;
+  p.v_cache = a->v_cache;
+  p.k_scale = a->k_scale;
+  p.v_scale = a->v_scale;
+  p.block_table = a->block_table;
+  p.seq_lens = a->seq_lens;
+  p.cu_tokens = a->cu_tokens;
+  p.positions = a->positions;
+  p.inv_freq = a->inv_freq;
+  p.err = dev.err_word;
+  p.T = a->T;
+  p.B = static_cast<int>(a->B);
+  p.Hq = static_cast<int>(Hq);
+  p.Hkv = static_cast<int>(a->Hkv);
+  p.half = static_cast<int>(a->rot_dim / 2);
+  p.interleaved = a->interleaved ? 1 : 0;
+  p.page_size = static_cast<int>(ps);
+  p.num_pages = static_cast<int>(a->num_pages);
+  p.max_pages = static_cast<int>(a->max_pages_per_seq);
+  p.block = static_cast<int>(fp8 ? a->scale_block : 16);
+  p.unit = std::max(p.block, 16);
+  p.per_seq = a->cu_tokens ? 0 : static_cast<int>(a->T / a->B);
+  // A run of n positions touches at most (n - 2 + unit) / unit + 1 units.
+  int64_t units;
+  if (p.per_seq) {
+    p.units_per_seq = (p.per_seq - 2 + p.unit) / p.unit + 1;
+    units = a->B * p.units_per_seq;
+  } else {
+    units = (a->T + p.unit - 1) / p.unit + std::min<int64_t>(a->B, a->T) * 2;
+  }
+  if (units > lim) return ATTN_ERR_INVALID_ARG;
+  // Few units: the heads are dealt over several CTAs of a unit, up to about two CTAs per SM.
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(a->Hkv, 2 * dev.sm_count / units));
+  const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>(parts));
+  const size_t smem = static_cast<size_t>(p.unit) * p.half * sizeof(float2);
+  if (a->d == 64) {
+    if (fp8) attn_append_kernel<64, true><<<grid, kAppThreads, smem, stream>>>(p);
+    else attn_append_kernel<64, false><<<grid, kAppThreads, smem, stream>>>(p);
+  } else {
+    if (fp8) attn_append_kernel<128, true><<<grid, kAppThreads, smem, stream>>>(p);
+    else attn_append_kernel<128, false><<<grid, kAppThreads, smem, stream>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" int attn_kv_append_debug_error(cudaStream_t stream, int* device_code) {
+  if (cudaStreamSynchronize(stream) != cudaSuccess) return ATTN_ERR_CUDA;
+  AppDevice dev;
+  const int st = app_device_setup(dev);
+  if (st != ATTN_OK) return st;
+  int code = 0;
+  if (cudaMemcpy(&code, dev.err_word, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return ATTN_ERR_CUDA;
+  const int zero = 0;
+  if (cudaMemcpy(dev.err_word, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (device_code) *device_code = code;
+  return code ? ATTN_ERR_INVALID_ARG : ATTN_OK;
+}

@@ -411,6 +411,80 @@ int attn_decode_static(const void* q, const void* k_cache, const void* v_cache, 
                        int64_t num_pages, int64_t page_size, int64_t max_pages_per_seq, int64_t num_splits,
                        float scale, int mask_kind, int64_t window, cudaStream_t stream);
 
+/*
+ * attn_kv_append: enqueue the write side of the paged cache on `stream`: the keys and values
+ * of new tokens go into their sequences' pages, the keys rotated by their positions on the
+ * way; the queries of the same tokens are rotated too and written where attn_decode (or
+ * attn_decode_kv8) reads them. (The pages name the cache and its pages, see attn_decode;
+ * how the cache is filled is not on them.)
+ *
+ * Rotation (rotary positions): with x the token's position and f_i = inv_freq[i], the pair
+ * (a, b) number i of a head's row becomes (a cos(x f_i) - b sin(x f_i), b cos(x f_i) + a sin(x f_i)).
+ * Pair i is elements (i, i + rot_dim / 2), or (2i, 2i + 1) with `interleaved`; elements from
+ * rot_dim on are copied. Angles are formed in fp64, the rotation is fp32, rounded once.
+ *
+ * Tokens are rows of q, k and v, sequence after sequence. With cu_tokens NULL every one of
+ * the B sequences has T / B rows; otherwise sequence b has rows cu_tokens[b] .. cu_tokens[b + 1]
+ * - 1 (none is fine), and rows from cu_tokens[B] on are not read. seq_lens counts the new
+ * tokens in, as in attn_decode: with n_b new tokens, they take positions seq_lens[b] - n_b ..
+ * seq_lens[b] - 1. Only the table entries of the pages they fall into are read, only their
+ * slots are written: every other slot of the cache keeps its bytes.
+ *
+ * 8-bit cache (scale_block != 0): slots hold E4M3 codes, and k_scale, v_scale
+ * [num_pages, Hkv, page_size / scale_block] hold one scale for each block of scale_block
+ * slots of a head: value = E4M3(code) * scale. A scale is the smallest power of two s >= 2^-40
+ * with amax <= 448 s over the block's new tokens (finite values; infinities become +-448 s,
+ * NaN stays NaN), and a code is x / s rounded to nearest even. A block that held tokens of the
+ * sequence before this call keeps its scale where its new tokens fit (amax <= 448 s);
+ * otherwise it takes theirs, and its older codes are rounded again under it (which changes
+ * their values only where they turn subnormal).
+ *
+ * Fields of the argument block (zero-initialise, then set what is needed):
+ *   k, v          device, bf16, T rows of [Hkv, d]; k_stride, v_stride elements from row to row
+ *                 (at least Hkv * d, a multiple of 8), 16-byte aligned: views of one projection's
+ *                 output will do
+ *   q, q_stride   device, bf16, T rows of [Hq, d], likewise; NULL: no queries
+ *   q_out         device, bf16, 16-byte aligned: [B, Hq, T / B, d] without cu_tokens, [T, Hq, d]
+ *                 with it; NULL exactly where q is
+ *   k_cache, v_cache  device, bf16 or E4M3 codes, [num_pages, Hkv, page_size, d], 16-byte aligned
+ *   k_scale, v_scale  device, fp32, as above; NULL exactly where scale_block is 0
+ *   block_table   device, int32, [B, max_pages_per_seq]
+ *   seq_lens      device, int32, [B]; n_b <= seq_lens[b] <= max_pages_per_seq * page_size
+ *   cu_tokens     device, int32, [B + 1], or NULL (T % B == 0)
+ *   positions     device, int32, [T]: the rotation's positions; NULL: the cache's positions
+ *   inv_freq      device, fp32, [rot_dim / 2]; NULL exactly where rot_dim is 0 (no rotation)
+ *   rot_dim       0 .. d, a multiple of 16;  d in {64, 128};  page_size in {16, 32, 64, 128, 256}
+ *   scale_block   0 (bf16 cache) or a power of two <= page_size
+ *
+ * A sequence whose length or row range is unusable is skipped, as are the cache rows of a page
+ * entry outside [0, num_pages); both are reported by attn_kv_append_debug_error as
+ * ATTN_ERR_INVALID_ARG. Two sequences of one call must not name the same page for new tokens.
+ * What is written must not overlap anything else (ATTN_ERR_INVALID_ARG). One launch; nothing
+ * is allocated and nothing synchronises; the result does not depend on any order of execution.
+ */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  void* q_out;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_tokens;
+  const int32_t* positions;
+  const float* inv_freq;
+  int64_t B, T, Hq, Hkv, d, rot_dim, num_pages, page_size, max_pages_per_seq, scale_block;
+  int interleaved;
+} attn_kv_append_args;
+int attn_kv_append(const attn_kv_append_args* args, cudaStream_t stream);
+/* attn_debug_error for the append's error word (one per device, shared like the forward's):
+   ATTN_ERR_INVALID_ARG for an unusable sequence or page-table entry. */
+int attn_kv_append_debug_error(cudaStream_t stream, int* device_code);
+
 #ifdef __cplusplus
 }
 #endif
