@@ -23,7 +23,9 @@ EXPORTS = ("attn_fwd", "attn_fwd_ex", "attn_status_string", "attn_debug_error", 
            "attn_bwd", "attn_bwd_ex", "attn_bwd_workspace_bytes", "attn_bwd_debug_error",
            "attn_decode", "attn_decode_ex", "attn_decode_workspace_bytes", "attn_decode_num_splits",
            "attn_decode_debug_error", "attn_fwd_fp8", "attn_fwd_fp8_ex", "attn_merge", "attn_fwd_host",
-           "attn_fwd_fp8_host", "attn_decode_static", "attn_kv_append", "attn_kv_append_debug_error")
+           "attn_fwd_fp8_host", "attn_decode_static", "attn_kv_append", "attn_kv_append_debug_error",
+           "attn_decode_kv8", "attn_decode_kv8_workspace_bytes", "attn_decode_kv8_num_splits",
+           "attn_decode_kv8_debug_error")
 
 _lib = None
 
@@ -113,6 +115,15 @@ def load_library():
     lib.attn_kv_append.restype = ctypes.c_int
     lib.attn_kv_append_debug_error.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
     lib.attn_kv_append_debug_error.restype = ctypes.c_int
+    lib.attn_decode_kv8.argtypes = [vp] * 10 + [ctypes.c_size_t] + [i64] * 10 + [f32, ctypes.c_int, i64, i64, vp,
+                                                                                  ctypes.POINTER(FwdOptions)]
+    lib.attn_decode_kv8.restype = ctypes.c_int
+    lib.attn_decode_kv8_workspace_bytes.argtypes = [i64] * 6
+    lib.attn_decode_kv8_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_decode_kv8_num_splits.argtypes = [i64] * 5 + [ctypes.c_int, i64, i64]
+    lib.attn_decode_kv8_num_splits.restype = i64
+    lib.attn_decode_kv8_debug_error.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
+    lib.attn_decode_kv8_debug_error.restype = ctypes.c_int
     lib.attn_merge.argtypes = [vp, vp, vp, vp, vp, i64, i64, ctypes.c_int, vp]
     lib.attn_merge.restype = ctypes.c_int
     _lib = lib
@@ -412,6 +423,109 @@ def decode_static(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     if st != 0:
         raise AttnError(st, "attn_decode_static")
     return out, lse
+
+
+def decode_kv8_num_splits(B, Hq, Hkv, Nq, max_seq_len, mask="causal", window=None, sinks=0) -> int:
+    """Suggested split count for a ``decode_kv8`` step (host-only; see include/attn.h)."""
+    if mask not in MASKS:
+        raise ValueError(f"mask must be one of {sorted(MASKS)}")
+    n = int(load_library().attn_decode_kv8_num_splits(B, Hq, Hkv, Nq, int(max_seq_len), MASKS[mask],
+                                                      int(window) if window is not None else 0, int(sinks)))
+    if n < 1:
+        raise ValueError("invalid decoding sizes")
+    return n
+
+
+def decode_kv8_workspace_bytes(B, Hq, Hkv, Nq, d, num_splits) -> int:
+    return int(load_library().attn_decode_kv8_workspace_bytes(B, Hq, Hkv, Nq, d, int(num_splits)))
+
+
+def decode_kv8_workspace(B, Hq, Hkv, Nq, d, num_splits, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for ``decode_kv8`` steps of these sizes, to keep from step to step
+    (one for each stream or captured graph that may run at the same time)."""
+    n = decode_kv8_workspace_bytes(B, Hq, Hkv, Nq, d, num_splits)
+    if n < 1:
+        raise ValueError("invalid decoding sizes")
+    return torch.zeros(n // 4, dtype=torch.float32, device=device)
+
+
+def decode_kv8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+               v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+               max_seq_len: Optional[int] = None, scale: Optional[float] = None, mask: str = "causal",
+               window: Optional[int] = None, sinks: int = 0, num_splits: Optional[int] = None,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+               wait_timeout_ns: int = 0, grid_ctas: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``decode`` over an 8-bit paged cache: k_cache/v_cache hold E4M3 codes (uint8 or
+    float8_e4m3fn, [num_pages,Hkv,page_size,d]) with one fp32 scale for each block of tokens
+    and head (k_scale/v_scale [num_pages,Hkv,page_size/block], as ``kv_append`` writes them).
+    With the sliding window, ``sinks`` first positions stay visible.  seq_lens[b] = 0 marks an
+    idle slot (out 0, lse -inf).  Returns (out bf16 [B,Hq,Nq,d], lse fp32 [B,Hq,Nq]).
+    """
+    lib = load_library()
+    _check(q, "q", torch.bfloat16, 4)
+    k_cache, v_cache = _codes(k_cache, "k_cache"), _codes(v_cache, "v_cache")
+    _check(k_scale, "k_scale", torch.float32, 3)
+    _check(v_scale, "v_scale", torch.float32, 3)
+    _check(block_table, "block_table", torch.int32, 2)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    B, Hq, Nq, d = q.shape
+    num_pages, Hkv, page_size, dk = k_cache.shape
+    if dk != d or v_cache.shape != k_cache.shape or block_table.shape[0] != B or seq_lens.shape[0] != B:
+        raise ValueError("q, cache, block_table and seq_lens shapes disagree")
+    per_page = k_scale.shape[2]
+    if k_scale.shape != v_scale.shape or tuple(k_scale.shape[:2]) != (num_pages, Hkv) or per_page < 1 \
+            or page_size % per_page:
+        raise ValueError("k_scale and v_scale must be [num_pages, Hkv, page_size / block]")
+    if mask not in MASKS:
+        raise ValueError(f"mask must be one of {sorted(MASKS)}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    max_pages = block_table.shape[1]
+    if num_splits is None:
+        num_splits = decode_kv8_num_splits(B, Hq, Hkv, Nq, max_pages * page_size if max_seq_len is None else max_seq_len,
+                                           mask, window, sinks)
+    device = q.device
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
+    _check(out, "out", torch.bfloat16, 4)
+    _check(lse, "lse", torch.float32, 3)
+    if out.shape != q.shape or tuple(lse.shape) != (B, Hq, Nq):
+        raise ValueError("out or lse has the wrong shape")
+    if workspace is None:
+        workspace = decode_kv8_workspace(B, Hq, Hkv, Nq, d, num_splits, device)
+    if not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if any(t.device != device for t in (k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse,
+                                        workspace)):
+        raise ValueError("all tensors must be on one device")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    opts = FwdOptions(int(wait_timeout_ns), 0, int(grid_ctas))
+    with torch.cuda.device(device):
+        st = lib.attn_decode_kv8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                 v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+                                 lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                 B, Hq, Hkv, Nq, d, num_pages, page_size, max_pages, page_size // per_page,
+                                 int(num_splits), float(scale), MASKS[mask],
+                                 int(window) if window is not None else 0, int(sinks),
+                                 ctypes.c_void_p(stream.cuda_stream), ctypes.byref(opts))
+    if st != 0:
+        raise AttnError(st, "attn_decode_kv8")
+    return out, lse
+
+
+def decode_kv8_debug_error(stream: Optional[torch.cuda.Stream] = None, device=None) -> Tuple[int, int]:
+    """Synchronise and read/clear the 8-bit decoding kernel's error word: (status, raw code)."""
+    lib = load_library()
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    code = ctypes.c_int(0)
+    with torch.cuda.device(stream.device):
+        st = lib.attn_decode_kv8_debug_error(ctypes.c_void_p(stream.cuda_stream), ctypes.byref(code))
+    return st, code.value
 
 
 def _rows(t: torch.Tensor, name: str, T, H, d):

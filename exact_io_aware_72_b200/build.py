@@ -10,8 +10,9 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libattn_b200.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("attn_fwd.cu", "attn_bwd.cu", "attn_decode.cu", "attn_merge.cu",
-                                                "attn_fwd_host.cu", "attn_append.cu")]
-HEADERS = [os.path.join(CSRC, f) for f in ("attn_fwd_kernel.cuh", "attn_bwd_kernel.cuh", "attn_decode_kernel.cuh", "sm100_ptx.cuh")] + [
+                                                "attn_fwd_host.cu", "attn_append.cu", "attn_decode8.cu")]
+HEADERS = [os.path.join(CSRC, f) for f in ("attn_fwd_kernel.cuh", "attn_bwd_kernel.cuh", "attn_decode_kernel.cuh",
+                                                "attn_decode8_kernel.cuh", "sm100_ptx.cuh")] + [
     os.path.join(ROOT, "include", "attn.h")]
 
 

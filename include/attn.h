@@ -485,6 +485,50 @@ int attn_kv_append(const attn_kv_append_args* args, cudaStream_t stream);
    ATTN_ERR_INVALID_ARG for an unusable sequence or page-table entry. */
 int attn_kv_append_debug_error(cudaStream_t stream, int* device_code);
 
+/*
+ * attn_decode_kv8: attn_decode over a cache held in 8 bits (as attn_kv_append writes it, or
+ * any E4M3 codes with scales). Cached values are E4M3(code) * scale, one scale for each block
+ * of scale_block slots of a page and head; the result is the exact masked softmax attention
+ * of those values for the bf16 queries. Half the bytes of the bf16 cache are read.
+ *
+ *   q, block_table, seq_lens, out, lse, num_splits, scale, window, stream: as attn_decode, and
+ *                     seq_lens[b] == 0 marks an idle slot of a padded batch: out 0, lse -inf,
+ *                     nothing of its table read, no error
+ *   k_cache, v_cache  device, E4M3 codes, [num_pages, Hkv, page_size, d], contiguous, 16-byte aligned
+ *   k_scale, v_scale  device, fp32, [num_pages, Hkv, page_size / scale_block], contiguous, 4-byte
+ *                     aligned; finite. V scales are meant to lie in [2^-40, 2^40]: one outside is
+ *                     taken as the nearest bound
+ *   scale_block       a power of two, at most page_size
+ *   mask_kind         as attn_decode
+ *   sinks             with ATTN_MASK_SLIDING_WINDOW: the first `sinks` positions stay visible
+ *                     (j < sinks, j <= the row's position) beside the window; 0 = none. Pages
+ *                     between the sinks and the oldest window position are neither looked up nor
+ *                     read. Must be 0 with the other masks
+ *   workspace         device, 16-byte aligned, attn_decode_kv8_workspace_bytes(B, Hq, Hkv, Nq, d,
+ *                     num_splits) bytes, with the contract of attn_decode's (first 256 bytes zero
+ *                     before the first call and after each; not shared by concurrent calls)
+ *   opts              wait bound and CTA count as for attn_fwd_ex; may be NULL
+ *
+ * Precision: the products take the codes exactly; a bf16 query row is split into two E4M3
+ * terms (exact to 2^-18 of the row's largest element); scores, statistics and sums are fp32;
+ * softmax weights go to the product with V as sums of three E5M2 numbers (9 significant bits,
+ * about bf16's); weights below 2^-28 of a row's largest are dropped there (and only there).
+ * Ownership, checks, overlap rules, bounded waits and errors as attn_decode.
+ */
+int attn_decode_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                    const float* v_scale, const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
+                    void* workspace, size_t workspace_bytes, int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq,
+                    int64_t d, int64_t num_pages, int64_t page_size, int64_t max_pages_per_seq, int64_t scale_block,
+                    int64_t num_splits, float scale, int mask_kind, int64_t window, int64_t sinks,
+                    cudaStream_t stream, const attn_fwd_options* opts);
+/* Workspace bytes attn_decode_kv8 needs (0 on invalid sizes). */
+size_t attn_decode_kv8_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d, int64_t num_splits);
+/* Suggested num_splits, as attn_decode_num_splits (-1 on invalid sizes). Host-only. */
+int64_t attn_decode_kv8_num_splits(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t max_seq_len, int mask_kind,
+                                   int64_t window, int64_t sinks);
+/* attn_decode_debug_error for the 8-bit decoding kernel's error word. */
+int attn_decode_kv8_debug_error(cudaStream_t stream, int* device_code);
+
 #ifdef __cplusplus
 }
 #endif
