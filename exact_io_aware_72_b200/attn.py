@@ -40,7 +40,8 @@ class FwdOptions(ctypes.Structure):
     """attn_fwd_options of include/attn.h."""
     _fields_ = [("wait_timeout_ns", ctypes.c_uint64), ("inject_stall", ctypes.c_int),
                 ("grid_ctas", ctypes.c_int), ("item_visits", ctypes.c_void_p), ("p_bf16", ctypes.c_int),
-                ("out_fp32", ctypes.c_int), ("key_offset", ctypes.c_int64), ("bwd_deterministic", ctypes.c_int)]
+                ("out_fp32", ctypes.c_int), ("key_offset", ctypes.c_int64), ("bwd_deterministic", ctypes.c_int),
+                ("sinks", ctypes.c_int64)]
 
 
 class KvAppendArgs(ctypes.Structure):
@@ -141,7 +142,7 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float
         mask: str = "causal", window: Optional[int] = None, out: Optional[torch.Tensor] = None,
         lse: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
         wait_timeout_ns: int = 0, inject_stall: bool = False, grid_ctas: int = 0, p_bf16: bool = False,
-        item_visits: Optional[torch.Tensor] = None, out_fp32: bool = False, key_offset: int = 0
+        item_visits: Optional[torch.Tensor] = None, out_fp32: bool = False, key_offset: int = 0, sinks: int = 0
         ) -> Tuple[torch.Tensor, torch.Tensor]:
     """Exact attention forward: returns (out bf16 [B,Hq,N,d], lse fp32 [B,Hq,N]).
 
@@ -153,6 +154,7 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float
     counters) is a test hook counting each work item's visits; ``out_fp32``
     returns out in fp32, unrounded (partial results to merge); ``key_offset``
     places query row i at key position i + key_offset (causal and window masks).
+    ``sinks`` first keys stay visible beside the sliding window.
     """
     lib = load_library()
     _check(q, "q", torch.bfloat16, 4)
@@ -181,7 +183,7 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float
             raise ValueError("item_visits must be a contiguous int32 CUDA tensor")
         visits = item_visits.data_ptr()
     opts = FwdOptions(int(wait_timeout_ns), 1 if inject_stall else 0, int(grid_ctas), visits, 1 if p_bf16 else 0,
-                      1 if out_fp32 else 0, int(key_offset))
+                      1 if out_fp32 else 0, int(key_offset), 0, int(sinks))
     with torch.cuda.device(q.device):
         st = lib.attn_fwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                              B, Hq, Hkv, N, d, float(scale), MASKS[mask],
@@ -202,11 +204,11 @@ def _codes(t: torch.Tensor, name: str) -> torch.Tensor:
 def fwd_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: float, k_scale: float, v_scale: float,
             scale: Optional[float] = None, mask: str = "causal", window: Optional[int] = None,
             out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-            stream: Optional[torch.cuda.Stream] = None, wait_timeout_ns: int = 0, grid_ctas: int = 0
+            stream: Optional[torch.cuda.Stream] = None, wait_timeout_ns: int = 0, grid_ctas: int = 0, sinks: int = 0
             ) -> Tuple[torch.Tensor, torch.Tensor]:
     """Exact attention forward of E4M3 inputs: q, k, v hold E4M3 codes (uint8 or
     torch.float8_e4m3fn, [B,H,N,128]) whose values are code * q_scale (k_scale,
-    v_scale); returns (out bf16 [B,Hq,N,128], lse fp32 [B,Hq,N])."""
+    v_scale); returns (out bf16 [B,Hq,N,128], lse fp32 [B,Hq,N]).  ``sinks`` as in ``fwd``."""
     lib = load_library()
     q, k, v = _codes(q, "q"), _codes(k, "k"), _codes(v, "v")
     B, Hq, N, d = q.shape
@@ -226,6 +228,7 @@ def fwd_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: float, k
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
     opts = FwdOptions(int(wait_timeout_ns), 0, int(grid_ctas))
+    opts.sinks = int(sinks)
     with torch.cuda.device(q.device):
         st = lib.attn_fwd_fp8_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), float(q_scale), float(k_scale),
                                  float(v_scale), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, N, d, float(scale),
@@ -241,9 +244,9 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ls
         dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
         workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
         wait_timeout_ns: int = 0, grid_ctas: int = 0,
-        deterministic: bool = False) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+        deterministic: bool = False, sinks: int = 0) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Exact attention backward: returns (dq, dk, dv), the gradients of
-    sum(dout * out) for the forward's q, k, v (same scale / mask / window).
+    sum(dout * out) for the forward's q, k, v (same scale / mask / window / sinks).
 
     ``out`` and ``lse`` are the forward's outputs for these inputs. The fp32
     workspace (allocated here when not given) holds the row terms
@@ -282,6 +285,7 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ls
         stream = torch.cuda.current_stream(q.device)
     opts = FwdOptions(int(wait_timeout_ns), 0, int(grid_ctas))
     opts.bwd_deterministic = int(bool(deterministic))
+    opts.sinks = int(sinks)
     with torch.cuda.device(q.device):
         st = lib.attn_bwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                              dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
@@ -322,7 +326,7 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
            mask: str = "causal", window: Optional[int] = None, num_splits: Optional[int] = None,
            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
            workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
-           wait_timeout_ns: int = 0, grid_ctas: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
+           wait_timeout_ns: int = 0, grid_ctas: int = 0, sinks: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
     """One decoding step against a paged KV cache: returns (out bf16 [B,Hq,Nq,d],
     lse fp32 [B,Hq,Nq]).
 
@@ -333,7 +337,8 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     of seq_lens, default max_pages*page_size) only picks the default
     ``num_splits``.  The workspace (work counter and the splits' partial
     results) is allocated here, zero-filled, when not given; a caller's own
-    workspace must start zeroed and is left with its counter at zero.
+    workspace must start zeroed and is left with its counter at zero.  With the
+    sliding window, ``sinks`` first positions stay visible.
     """
     lib = load_library()
     _check(q, "q", torch.bfloat16, 4)
@@ -370,7 +375,7 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     ws_ptr, ws_len = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
-    opts = FwdOptions(int(wait_timeout_ns), 0, int(grid_ctas), None, 0, 0, 0)
+    opts = FwdOptions(int(wait_timeout_ns), 0, int(grid_ctas), None, 0, 0, 0, 0, int(sinks))
     with torch.cuda.device(q.device):
         st = lib.attn_decode_ex(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                 seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), ws_ptr, ws_len,

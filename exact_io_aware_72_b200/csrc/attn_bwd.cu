@@ -153,6 +153,8 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
   if (mask_kind != ATTN_MASK_FULL && mask_kind != ATTN_MASK_CAUSAL && mask_kind != ATTN_MASK_SLIDING_WINDOW)
     return ATTN_ERR_INVALID_ARG;
   if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window < 1) return ATTN_ERR_INVALID_ARG;
+  const int64_t sinks = std::min<int64_t>(opts ? opts->sinks : 0, N);
+  if (sinks < 0 || (sinks > 0 && mask_kind != ATTN_MASK_SLIDING_WINDOW)) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   // Byte counts must fit in 63 bits (B * Hq * N <= 2^60 after sizes_ok).
@@ -197,7 +199,7 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
     return ATTN_ERR_CUDA;
   int kind = mask_kind;
   int64_t w = window;
-  if (kind == ATTN_MASK_SLIDING_WINDOW && w >= N) kind = ATTN_MASK_CAUSAL;  // a window covering everything
+  if (kind == ATTN_MASK_SLIDING_WINDOW && w >= N - sinks) kind = ATTN_MASK_CAUSAL;  // everything earlier is visible
   p.lse = lse;
   p.delta = static_cast<const float*>(workspace);
   p.dq = static_cast<__nv_bfloat16*>(dq);
@@ -211,6 +213,7 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
   p.group = static_cast<int>(Hq / Hkv);
   p.mask_kind = kind;
   p.window = static_cast<int>(kind == ATTN_MASK_SLIDING_WINDOW ? w : N);
+  p.sinks = static_cast<int>(kind == ATTN_MASK_SLIDING_WINDOW ? sinks : 0);
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.num_blk = static_cast<int>((N + kTile - 1) / kTile);

@@ -74,6 +74,7 @@ struct BwdParams {
   int* err;           // device error word (shared with the forward)
   int B, Hq, Hkv, N, group;
   int mask_kind, window;
+  int sinks;          // window mask: keys below it stay visible to every later query
   float scale;        // softmax scale (dQ, dK are scaled by it)
   float scale_log2;   // scale * log2(e)
   int num_blk;        // ceil(N / 128)
@@ -81,8 +82,9 @@ struct BwdParams {
   unsigned long long timeout_ns;
 };
 
-// Visible key range [lo, hi] (tile indices) of query tile m, and visible query
-// tile range of key tile n (the transposed question), for the three masks.
+// Visible key range [lo, hi] (tile indices) of query tile m (its window: sink tiles
+// before lo come on top, see DqItem), and visible query tile range of key tile n (the
+// transposed question), for the three masks.
 __device__ __forceinline__ void key_tiles_of_query_tile(const BwdParams& p, int m, int& lo, int& hi) {
   const int r0 = m * kTile;
   const int r1 = min(r0 + kTile - 1, p.N - 1);
@@ -103,7 +105,9 @@ __device__ __forceinline__ void query_tiles_of_key_tile(const BwdParams& p, int 
   } else {
     lo = c0 / kTile;  // query i sees key j only if j <= i
     // window: key j is seen by queries i with j <= i <= j + w - 1
-    hi = (p.mask_kind == kBMaskWindow) ? min(p.num_blk - 1, (c1 + p.window - 1) / kTile) : p.num_blk - 1;
+    // (a sink by all from j on)
+    hi = (p.mask_kind == kBMaskWindow && c0 >= p.sinks) ? min(p.num_blk - 1, (c1 + p.window - 1) / kTile)
+                                                        : p.num_blk - 1;
   }
 }
 // Does the (query tile m, key tile n) block need element masks?
@@ -111,7 +115,7 @@ __device__ __forceinline__ bool block_is_partial(const BwdParams& p, int m, int 
   const int r0 = m * kTile, c0 = n * kTile;
   bool partial = (c0 + kTile > p.N) || (r0 + kTile > p.N);
   if (p.mask_kind != kBMaskFull) partial |= (c0 + kTile - 1 > r0);
-  if (p.mask_kind == kBMaskWindow) partial |= (c0 <= r0 + kTile - 1 - p.window);
+  if (p.mask_kind == kBMaskWindow) partial |= (c0 <= r0 + kTile - 1 - p.window) && c0 + kTile > p.sinks;
   return partial;
 }
 
@@ -304,6 +308,8 @@ __device__ __forceinline__ void store_acc_row(uint32_t tacc, float mul, __nv_bfl
 // ------------------------------------------------------------------ query-tile work items and loader
 struct DqItem {
   int b, hq, hkv, m, lo, hi;
+  int ns;  // sink tiles before lo: the item's steps are u = lo - ns .. hi
+  __device__ __forceinline__ int tile(int u) const { return u < lo ? u - (lo - ns) : u; }
 };
 __device__ __forceinline__ DqItem dq_item(const BwdParams& p, int i) {
   DqItem it;
@@ -313,6 +319,7 @@ __device__ __forceinline__ DqItem dq_item(const BwdParams& p, int i) {
   it.hq = bh - it.b * p.Hq;
   it.hkv = it.hq / p.group;
   key_tiles_of_query_tile(p, it.m, it.lo, it.hi);
+  it.ns = min((p.sinks + kTile - 1) / kTile, it.lo);
   return it;
 }
 
@@ -342,7 +349,8 @@ __device__ __forceinline__ void dq_loader(const BwdParams& p, uint32_t sbase, co
                   it.m * kTile, zq, pol_q);
     }
     const int zk = it.b * p.Hkv + it.hkv;
-    for (int j = it.lo; j <= it.hi; ++j, ++n) {
+    for (int u = it.lo - it.ns; u <= it.hi; ++u, ++n) {
+      const int j = it.tile(u);
       const uint32_t slot = n % L::kStages;
       if (n >= (uint32_t)L::kStages &&
           !w.wait(bar(L::kRingEmpty + slot), ((n / L::kStages) - 1) & 1,
@@ -647,7 +655,7 @@ __device__ __forceinline__ void dkv_elem(const BwdParams& p, uint32_t sbase, uin
         // (applied on partial tiles, where masked scores become -inf).
         const int q0 = m * kTile + h * kHalf;
         const int hi_c =
-            (key < p.N) ? min(p.N - 1, p.mask_kind == kBMaskWindow ? key + p.window - 1 : p.N - 1) - q0 : -1;
+            (key < p.N) ? min(p.N - 1, p.mask_kind == kBMaskWindow && key >= p.sinks ? key + p.window - 1 : p.N - 1) - q0 : -1;
         const int lo_c = (p.mask_kind == kBMaskFull) ? 0 : key - q0;
         const uint32_t t_s = tmem + lane_bits + L::col_s(h), t_p = tmem + lane_bits + L::col_p(h);
         uint32_t pk[2][16], dk[2][16];
@@ -766,7 +774,7 @@ __device__ __forceinline__ void dqf_mma(const BwdParams& p, uint32_t sbase, uint
     const DqItem it = dq_item(p, i);
     if (!w.wait_warp(bar(L::kFixFull), items & 1, code | L::kFixFull)) break;
     tc_fence_after_sync();
-    for (int j = it.lo; j <= it.hi; ++j, ++g) {
+    for (int u = it.lo - it.ns; u <= it.hi; ++u, ++g) {
       const uint32_t slot = g % L::kStages;
       if (!w.wait_warp(bar(L::kRingFull + slot), (g / L::kStages) & 1, code | (L::kRingFull + slot)) ||
           (g > 0 && !w.wait_warp(bar(kXFree), (g - 1) & 1, code | kXFree))) {
@@ -792,11 +800,11 @@ __device__ __forceinline__ void dqf_mma(const BwdParams& p, uint32_t sbase, uint
         mma_bf16_ss_elect(tY, do_desc + off, v_desc + off, idesc_ss, kk > 0 ? 1u : 0u);
       }
       tc_commit_elect(bar(kDpFull));
-      if (j == it.hi) tc_commit_elect(bar(L::kFixEmpty));  // Q and dO read by the item's last products
+      if (u == it.hi) tc_commit_elect(bar(L::kFixEmpty));  // Q and dO read by the item's last products
       pend = true;
       pend_slot = slot;
-      pend_first = (j == it.lo);
-      pend_last = (j == it.hi);
+      pend_first = (u == it.lo - it.ns);
+      pend_last = (u == it.hi);
     }
   }
   if (ok && pend) issue_b();
@@ -825,7 +833,8 @@ __device__ __forceinline__ void dqf_elem(const BwdParams& p, uint32_t sbase, uin
     const float dlt = row_ok ? p.delta[bhrow] : 0.f;
     const uint64_t c2x2 = f32x2_pack(c2, c2), nlse2x2 = f32x2_pack(-lse2, -lse2), ndlt2 = f32x2_pack(-dlt, -dlt);
     bool ok = true;
-    for (int j = it.lo; j <= it.hi && ok; ++j, ++g) {
+    for (int u = it.lo - it.ns; u <= it.hi && ok; ++u, ++g) {
+      const int j = it.tile(u);
       if (!w.wait_warp(bar(kSFull), g & 1, code | kSFull)) {
         ok = false;
         break;
@@ -841,9 +850,10 @@ __device__ __forceinline__ void dqf_elem(const BwdParams& p, uint32_t sbase, uin
         const int j0 = j * kTile;
         const int hi_c = row_ok ? min(p.N - 1, p.mask_kind == kBMaskFull ? p.N - 1 : row) - j0 : -1;
         const int lo_c = (p.mask_kind == kBMaskWindow) ? row - p.window + 1 - j0 : 0;
+        const int sink_c = p.sinks - j0;  // columns below it are sinks
 #pragma unroll
         for (int c = 0; c < kTile; ++c)
-          if (c > hi_c || c < lo_c) sv[c] = 0xff800000u;  // -inf
+          if (c > hi_c || (c < lo_c && c >= sink_c)) sv[c] = 0xff800000u;  // -inf
       }
       uint32_t pk[kTile / 2];  // P, bf16 pairs of keys
 #pragma unroll
@@ -1075,7 +1085,7 @@ __device__ __forceinline__ void dkvf_elem(const BwdParams& p, uint32_t sbase, ui
         // Query columns that see this key: lo_c <= c <= hi_c.
         const int q0 = m * kTile;
         const int hi_c =
-            (key < p.N) ? min(p.N - 1, p.mask_kind == kBMaskWindow ? key + p.window - 1 : p.N - 1) - q0 : -1;
+            (key < p.N) ? min(p.N - 1, p.mask_kind == kBMaskWindow && key >= p.sinks ? key + p.window - 1 : p.N - 1) - q0 : -1;
         const int lo_c = (p.mask_kind == kBMaskFull) ? 0 : key - q0;
 #pragma unroll
         for (int c = 0; c < kTile; ++c)

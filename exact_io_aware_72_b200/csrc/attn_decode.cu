@@ -177,6 +177,8 @@ extern "C" int attn_decode_ex(const void* q, const void* k_cache, const void* v_
   if (num_splits < 1 || num_splits > kMaxSplits) return ATTN_ERR_INVALID_ARG;
   if (mask_kind < ATTN_MASK_FULL || mask_kind > ATTN_MASK_SLIDING_WINDOW) return ATTN_ERR_INVALID_ARG;
   if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window < 1) return ATTN_ERR_INVALID_ARG;
+  const int64_t sinks = opts ? opts->sinks : 0;
+  if (sinks < 0 || (sinks > 0 && mask_kind != ATTN_MASK_SLIDING_WINDOW)) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
@@ -272,6 +274,7 @@ extern "C" int attn_decode_ex(const void* q, const void* k_cache, const void* v_
   p.num_pages = static_cast<int>(num_pages);
   p.mask_kind = mask_kind;
   p.window = static_cast<int>(std::min<int64_t>(window, int64_t(1) << 30));
+  p.sinks = static_cast<int>(std::min<int64_t>(sinks, int64_t(1) << 30));
   p.num_splits = static_cast<int>(num_splits);
   p.num_items = static_cast<int>(items);
   p.scale_log2 = scale * 1.4426950408889634f;

@@ -22,8 +22,8 @@
 //   scalars, and no thread computes an exponential that no row needs.
 // * O^T = V^T P^T (d x NR): A is the V tile read MN-major, B is P written to shared memory by
 //   the softmax threads, 16 rows (16 bytes) per key.  E4M3 V needs an 8-bit P: the weight is
-//   held as a sum of three E5M2 numbers (3 significant bits each, 9 together, an error of at
-//   most 2^-9 as for bf16 weights), three products into one accumulator.  Weights are
+//   held as a sum of three E5M2 numbers (3 significant bits each, 9 together: off by at most
+//   2^-9, half of a bf16 weight's rounding), three products into one accumulator.  Weights are
 //   scaled so that m sits at 2^11: they reach 2^15 before m must move (E5M2 ends at 57344),
 //   and a weight is lost only below 2^-28 of the largest.
 // * Sums l and all statistics are fp32; out is rounded once to bf16.

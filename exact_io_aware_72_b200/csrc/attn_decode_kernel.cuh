@@ -33,8 +33,8 @@
 //   loader warp's lanes in parallel; the page-table entries are read one tile
 //   ahead.  Boxes that hold no position of the step's visible range are not
 //   loaded at all; under a sliding window the pages wholly before the oldest
-//   visible key are never looked up, so a caller may recycle them (a rolling
-//   window buffer).  Rows of an edge tile outside the visible range are
+//   visible key (but for the sinks') are never looked up, so a caller may
+//   recycle them (a rolling window buffer).  Rows of an edge tile outside the visible range are
 //   cleared in shared memory before the P V MMA (those slots may hold
 //   anything), and masked scores are replaced by -inf.
 //
@@ -95,6 +95,7 @@ struct DecParams {
   int row_chunks;         // ceil(rows_total / rows_chunk)
   int page_size, rows_per_load, loads_per_tile, max_pages, num_pages;
   int mask_kind, window;
+  int sinks;              // window: positions below it stay visible
   int num_splits, num_items;
   float scale_log2;       // scale * log2(e)
   unsigned long long timeout_ns;
@@ -138,11 +139,20 @@ struct DecSmem {
 };
 
 // ------------------------------------------------------------ work items
+// Tiles are numbered t = 0, 1, ... over what the step can see: first the ns tiles that hold
+// sinks before the window's first tile, then the window's (without sinks t - ns + first is
+// simply the tile's place among the window's).
 struct DecItem {
   int b, hkv, rc, s;
   int L;        // cached keys of the sequence
-  int lo_pos;   // oldest position any query of the step can see
+  int lo_pos;   // oldest position any query's window can see
+  int sinks;    // positions below it are visible too
+  int ns, first;
   int t0, t1;   // tile range of this split (empty when t1 < t0)
+  __device__ __forceinline__ int tile(int t) const { return t < ns ? t : t - ns + first; }
+  __device__ __forceinline__ bool unseen(int pos0, int n) const {  // no position of [pos0, pos0 + n) is seen
+    return pos0 >= L || (pos0 + n <= lo_pos && pos0 >= sinks);
+  }
   int row0;     // first query row of the group handled here
   int rows;     // rows handled here
   bool bad;     // seq_lens[b] unusable: the item is empty and reports an error
@@ -160,14 +170,19 @@ __device__ __forceinline__ DecItem dec_item(const DecParams& p, int idx) {
   it.bad = it.L < p.Nq || it.L > p.max_pages * p.page_size;
   it.row0 = it.rc * p.rows_chunk;
   it.rows = min(p.rows_chunk, p.rows_total - it.row0);
-  it.lo_pos = 0;
+  it.lo_pos = it.sinks = it.ns = it.first = 0;
   it.t0 = 0;
   it.t1 = -1;
   if (!it.bad) {
-    if (p.mask_kind == kDMaskWindow) it.lo_pos = max(0, it.L - p.Nq - p.window + 1);
-    const int first = it.lo_pos / kKeys, last = (it.L - 1) / kKeys;
-    const int chunk = (last - first + p.num_splits) / p.num_splits;  // ceil(tiles / splits)
-    it.t0 = first + it.s * chunk;
+    if (p.mask_kind == kDMaskWindow) {
+      it.lo_pos = max(0, it.L - p.Nq - p.window + 1);
+      it.sinks = min(p.sinks, it.L);
+      it.first = it.lo_pos / kKeys;
+      it.ns = min((it.sinks + kKeys - 1) / kKeys, it.first);
+    }
+    const int last = (it.L - 1) / kKeys - it.first + it.ns;
+    const int chunk = (last + p.num_splits) / p.num_splits;  // ceil(tiles / splits)
+    it.t0 = it.s * chunk;
     it.t1 = min(last, it.t0 + chunk - 1);
   }
   return it;
@@ -301,13 +316,13 @@ __device__ __forceinline__ uint32_t dec_loader(const DecParams& p, uint32_t sbas
     // when used, so the table's load latency stays off the issue path.
     auto box_entry = [&](int t) -> int {
       if (t > it.t1 || lane >= p.loads_per_tile) return -1;
-      const int pos0 = t * kKeys + lane * p.rows_per_load;
-      if (pos0 >= it.L || pos0 + p.rows_per_load <= it.lo_pos) return -1;
+      const int pos0 = it.tile(t) * kKeys + lane * p.rows_per_load;
+      if (it.unseen(pos0, p.rows_per_load)) return -1;
       return __ldg(trow + pos0 / p.page_size);
     };
     auto checked = [&](int t, int entry) -> int {
-      const int pos0 = t * kKeys + lane * p.rows_per_load;
-      if (lane >= p.loads_per_tile || pos0 >= it.L || pos0 + p.rows_per_load <= it.lo_pos) return -1;
+      const int pos0 = it.tile(t) * kKeys + lane * p.rows_per_load;
+      if (lane >= p.loads_per_tile || it.unseen(pos0, p.rows_per_load)) return -1;
       if (entry < 0 || entry >= p.num_pages) {
         atomicCAS(p.err, 0, kDErrPage | (it.b & 0xFFFFF));
         return 0;  // stand-in inside the pool; the step's result is then undefined
@@ -326,7 +341,7 @@ __device__ __forceinline__ uint32_t dec_loader(const DecParams& p, uint32_t sbas
                               __popc(boxes) * static_cast<uint32_t>(p.rows_per_load) * 128u * L::kChunks);
       __syncwarp();
       if (page >= 0) {
-        const int y = (t * kKeys + lane * p.rows_per_load) % p.page_size;  // 0 unless pages exceed a tile
+        const int y = (it.tile(t) * kKeys + lane * p.rows_per_load) % p.page_size;  // 0 unless pages exceed a tile
         const int z = page * p.Hkv + it.hkv;
         const uint32_t tile = sbase + L::kRingOff + slot * L::kTileBytes;
         if (kv) {
@@ -564,7 +579,7 @@ __device__ __forceinline__ void dec_softmax(const DecParams& p, uint32_t sbase, 
       continue;
     }
     const int n = it.t1 - it.t0 + 1;
-    int lo_vis = 0, hi_vis = -1;  // visible key positions of this lane's row
+    int lo_vis = 0, hi_vis = -1;  // visible key positions of this lane's row, and those below sinks
     if (r < it.rows) {
       const int qpos = it.L - p.Nq + (it.row0 + r) % p.Nq;
       hi_vis = (p.mask_kind == kDMaskFull) ? it.L - 1 : qpos;
@@ -573,7 +588,7 @@ __device__ __forceinline__ void dec_softmax(const DecParams& p, uint32_t sbase, 
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
       const uint32_t gi = g + j;
-      const int base = (it.t0 + j) * kKeys;
+      const int base = it.tile(it.t0 + j) * kKeys;
       if (!w.wait_warp(bar(L::kSFull + (gi & 1)), (gi >> 1) & 1, code | (L::kSFull + (gi & 1)))) {
         ok = false;
         break;
@@ -593,11 +608,12 @@ __device__ __forceinline__ void dec_softmax(const DecParams& p, uint32_t sbase, 
         const int key0 = base + copy * C;
 #pragma unroll
         for (int c = 0; c < C; ++c) x[c] = __uint_as_float(sr[c]) * p.scale_log2;
-        if (!(key0 >= lo_vis && key0 + C - 1 <= hi_vis)) {
+        if (!((key0 >= lo_vis || key0 + C <= it.sinks) && key0 + C - 1 <= hi_vis)) {
           // Masked scores are replaced (not offset), so whatever an unloaded
           // or stale slot produced never reaches P.
 #pragma unroll
-          for (int c = 0; c < C; ++c) x[c] = (key0 + c >= lo_vis && key0 + c <= hi_vis) ? x[c] : -INFINITY;
+          for (int c = 0; c < C; ++c)
+            x[c] = ((key0 + c >= lo_vis || key0 + c < it.sinks) && key0 + c <= hi_vis) ? x[c] : -INFINITY;
         }
       }
       float mx = x[0];
@@ -655,22 +671,23 @@ __device__ __forceinline__ void dec_softmax(const DecParams& p, uint32_t sbase, 
           tmem_store_32cols(p_addr + c, part);
         }
       }
-      if (base < it.lo_pos || base + kKeys > it.L) {
-        // Edge tile: V rows outside [lo_pos, L) were not loaded or hold
-        // slots past the sequence end; P is zero there, and they are cleared
-        // so that 0 * (whatever they hold) cannot reach O.
+      if ((base < it.lo_pos && base + kKeys > it.sinks) || base + kKeys > it.L) {
+        // Edge tile: V rows in [sinks, lo_pos) or from L on were not loaded or
+        // hold anything; P is zero there, and they are cleared so that
+        // 0 * (whatever they hold) cannot reach O.
         const uint32_t vidx = 2 * gi + 1, vslot = vidx % L::kStages;
         if (!w.wait_warp(bar(L::kKVFull + vslot), (vidx / L::kStages) & 1, code | (L::kKVFull + vslot))) {
           ok = false;
           break;
         }
-        const int z0 = max(0, min(kKeys, it.lo_pos - base));  // rows [0, z0)
-        const int z1 = max(0, min(kKeys, it.L - base));       // rows [z1, 128)
+        const int za = max(0, min(kKeys, it.sinks - base));
+        const int z0 = max(0, min(kKeys, it.lo_pos - base) - za);  // rows [za, za + z0)
+        const int z1 = max(za + z0, min(kKeys, it.L - base));      // rows [z1, 128)
         const int nrows = z0 + (kKeys - z1);
         uint4* vt = reinterpret_cast<uint4*>(smem + L::kRingOff + vslot * L::kTileBytes);
         for (int e = tid; e < nrows * 8 * L::kChunks; e += kLanes) {
           const int rr = e / (8 * L::kChunks), rem = e - rr * (8 * L::kChunks);
-          const int row = rr < z0 ? rr : z1 + (rr - z0);
+          const int row = rr < z0 ? za + rr : z1 + (rr - z0);
           const int R = p.rows_per_load;
           vt[((row / R) * R * 128 * L::kChunks + (rem >> 3) * R * 128 + (row % R) * 128) / 16 + (rem & 7)] =
               make_uint4(0u, 0u, 0u, 0u);

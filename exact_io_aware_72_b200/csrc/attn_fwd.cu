@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -52,6 +53,18 @@ struct DeviceInfo {
 std::mutex g_dev_mutex;
 DeviceInfo g_dev[kMaxDevices];
 
+template <bool SINK>
+bool set_smem() {
+  auto set = [](auto kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+  };
+  return set(attn_fwd_kernel<64, 2, true, SINK>, SmemLayout<64>::kAlloc) &&
+         set(attn_fwd_kernel<128, 2, true, SINK>, SmemLayout<128>::kAlloc) &&
+         set(attn_fwd_kernel<128, 1, false, SINK>, SmemLayout<128, 1>::kAlloc) &&
+         set(attn_fwd_kernel<64, 2, false, SINK>, SmemLayout<64>::kAlloc) &&
+         set(attn_fwd_kernel<128, 2, false, SINK>, SmemLayout<128>::kAlloc);
+}
+
 // Probe the current device once: sm_100 check, SM count, error-word address,
 // and the dynamic shared-memory opt-in of every kernel instance.
 int device_setup(int& dev, DeviceInfo& out_info) {
@@ -71,16 +84,7 @@ int device_setup(int& dev, DeviceInfo& out_info) {
       void* addr = nullptr;
       if (cudaGetSymbolAddress(&addr, g_attn_error) != cudaSuccess) return ATTN_ERR_CUDA;
       info.err_word = static_cast<int*>(addr);
-      if (cudaFuncSetAttribute(attn_fwd_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               SmemLayout<64>::kAlloc) != cudaSuccess ||
-          cudaFuncSetAttribute(attn_fwd_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               SmemLayout<128>::kAlloc) != cudaSuccess ||
-          cudaFuncSetAttribute(attn_fwd_kernel<128, 1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               SmemLayout<128, 1>::kAlloc) != cudaSuccess ||
-          cudaFuncSetAttribute(attn_fwd_kernel<64, 2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               SmemLayout<64>::kAlloc) != cudaSuccess ||
-          cudaFuncSetAttribute(attn_fwd_kernel<128, 2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               SmemLayout<128>::kAlloc) != cudaSuccess)
+      if (!set_smem<false>() || !set_smem<true>())
         return ATTN_ERR_CUDA;
     }
     info.probed = true;
@@ -96,20 +100,21 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 
 struct Plan {
   int mask_kind;
-  int64_t window;
+  int64_t window, sinks;
   int pair_heads;
   int64_t num_mblk, row_units, head_units, num_items, super_items;
 };
 
 // Checks that need no device; fills the schedule plan.
 int check_sizes(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t d, int mask_kind, int64_t window,
-                Plan& plan, int64_t key_offset = 0) {
+                Plan& plan, int64_t key_offset = 0, int64_t sinks = 0) {
   if (B < 1 || Hq < 1 || Hkv < 1 || N < 1) return ATTN_ERR_INVALID_ARG;
   if (Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
   if (mask_kind != ATTN_MASK_FULL && mask_kind != ATTN_MASK_CAUSAL && mask_kind != ATTN_MASK_SLIDING_WINDOW)
     return ATTN_ERR_INVALID_ARG;
   if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window < 1) return ATTN_ERR_INVALID_ARG;
   if (key_offset < 0 || key_offset > (int64_t(1) << 30)) return ATTN_ERR_INVALID_ARG;
+  if (sinks < 0 || (sinks > 0 && mask_kind != ATTN_MASK_SLIDING_WINDOW)) return ATTN_ERR_INVALID_ARG;
   // Index arithmetic in the kernel is 32-bit for rows and heads.
   if (N > (int64_t(1) << 30) || B * Hq > (int64_t(1) << 30) || B * Hkv > (int64_t(1) << 30))
     return ATTN_ERR_INVALID_ARG;
@@ -119,10 +124,12 @@ int check_sizes(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t d, int ma
   if (B * Hq * N > (int64_t(1) << 61) / (d * 4)) return ATTN_ERR_INVALID_ARG;
   plan.mask_kind = mask_kind;
   plan.window = window;
-  // A window covering every earlier key is plain causal attention.
-  if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window >= N + key_offset) {
+  // A window covering every earlier key, with the sinks or without, is plain causal attention.
+  plan.sinks = std::min(sinks, N);
+  if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window >= N + key_offset - plan.sinks) {
     plan.mask_kind = ATTN_MASK_CAUSAL;
     plan.window = N;
+    plan.sinks = 0;
   }
   const int64_t group = Hq / Hkv;
   plan.pair_heads = (group % 2 == 0) ? 1 : 0;
@@ -148,6 +155,22 @@ CUresult encode_bhnd(EncodeTiledFn enc, CUtensorMap* map, const void* base, int6
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+template <bool SINK>
+cudaError_t launch_fwd(cudaLaunchConfig_t& cfg, const FwdParams& p, int eb, int64_t d, bool p_bf16) {
+  if (eb == 1) {
+    cfg.dynamicSmemBytes = SmemLayout<128, 1>::kAlloc;
+    return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<128, 1, false, SINK>, p);
+  }
+  if (d == 128) {
+    cfg.dynamicSmemBytes = SmemLayout<128>::kAlloc;
+    return p_bf16 ? cudaLaunchKernelEx(&cfg, attn_fwd_kernel<128, 2, false, SINK>, p)
+                  : cudaLaunchKernelEx(&cfg, attn_fwd_kernel<128, 2, true, SINK>, p);
+  }
+  cfg.dynamicSmemBytes = SmemLayout<64>::kAlloc;
+  return p_bf16 ? cudaLaunchKernelEx(&cfg, attn_fwd_kernel<64, 2, false, SINK>, p)
+                : cudaLaunchKernelEx(&cfg, attn_fwd_kernel<64, 2, true, SINK>, p);
+}
+
 // Shared by the bf16 (eb = 2) and E4M3 (eb = 1) entry points: checks, tensor
 // maps and the launch.  score_scale multiplies q.k of the stored values
 // (softmax scale, times the q and k scales for E4M3); v_scale multiplies O.
@@ -157,7 +180,7 @@ int fwd_launch(const void* q, const void* k, const void* v, void* out, float* ls
   if (!q || !k || !v || !out || !lse) return ATTN_ERR_INVALID_ARG;
   Plan plan{};
   const int64_t key_offset = opts ? opts->key_offset : 0;
-  int st = check_sizes(B, Hq, Hkv, N, d, mask_kind, window, plan, key_offset);
+  int st = check_sizes(B, Hq, Hkv, N, d, mask_kind, window, plan, key_offset, opts ? opts->sinks : 0);
   if (st != ATTN_OK) return st;
   if (eb == 1 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (!std::isfinite(score_scale) || !(score_scale > 0.f) || !std::isfinite(v_scale) || !(v_scale > 0.f))
@@ -201,6 +224,8 @@ int fwd_launch(const void* q, const void* k, const void* v, void* out, float* ls
   p.mask_kind = plan.mask_kind;
   p.window = static_cast<int>(plan.mask_kind == ATTN_MASK_SLIDING_WINDOW ? std::min<int64_t>(plan.window, 1 << 30) : N);
   p.key_offset = plan.mask_kind == ATTN_MASK_FULL ? 0 : static_cast<int>(key_offset);
+  p.sinks = static_cast<int>(plan.sinks);
+  p.sink_tiles = (p.sinks + kBlockN - 1) / kBlockN;
   p.scale_log2 = score_scale * 1.4426950408889634f;
   p.v_scale = v_scale;
   p.pair_heads = plan.pair_heads;
@@ -222,19 +247,7 @@ int fwd_launch(const void* q, const void* k, const void* v, void* out, float* ls
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
-  cudaError_t e;
-  if (eb == 1) {
-    cfg.dynamicSmemBytes = SmemLayout<128, 1>::kAlloc;
-    e = cudaLaunchKernelEx(&cfg, attn_fwd_kernel<128, 1, false>, p);
-  } else if (d == 128) {
-    cfg.dynamicSmemBytes = SmemLayout<128>::kAlloc;
-    e = p_bf16 ? cudaLaunchKernelEx(&cfg, attn_fwd_kernel<128, 2, false>, p)
-               : cudaLaunchKernelEx(&cfg, attn_fwd_kernel<128, 2, true>, p);
-  } else {
-    cfg.dynamicSmemBytes = SmemLayout<64>::kAlloc;
-    e = p_bf16 ? cudaLaunchKernelEx(&cfg, attn_fwd_kernel<64, 2, false>, p)
-               : cudaLaunchKernelEx(&cfg, attn_fwd_kernel<64, 2, true>, p);
-  }
+  const cudaError_t e = p.sinks ? launch_fwd<true>(cfg, p, eb, d, p_bf16) : launch_fwd<false>(cfg, p, eb, d, p_bf16);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -107,6 +107,8 @@ struct FwdParams {
   int mask_kind;
   int window;
   int key_offset;    // query row i sits at key position i + key_offset (causal and window masks)
+  int sinks;         // SINK kernels (window mask): keys below it stay visible
+  int sink_tiles;    // ceil(sinks / 128)
   float scale_log2;  // scale * log2(e)
   int pair_heads;    // 1: the two tiles are two heads of one KV group
   int num_mblk;      // ceil(N / 128)
@@ -160,6 +162,11 @@ struct WorkItem {
   int valid[2];
   int lo[2], hi[2];  // KV tile range of each query tile
   int lo_u, hi_u;    // union of the two ranges
+  int ns;            // SINK kernels: sink tiles before lo_u
+  // An item's steps are u = first_u() .. hi_u: the sink tiles 0 .. ns - 1, then tiles lo_u ..
+  // hi_u under their own numbers.  Without sinks u is the tile.
+  __device__ __forceinline__ int first_u() const { return lo_u - ns; }
+  __device__ __forceinline__ int tile(int u) const { return u < lo_u ? u - (lo_u - ns) : u; }
 };
 
 // Row r sees keys [r + key_offset - window + 1, r + key_offset] (window), keys
@@ -182,6 +189,7 @@ __device__ __forceinline__ void kv_range(const FwdParams& p, int m, int& lo, int
 // Work item (head unit hu, row unit r): head unit = (b, query head) or
 // (b, query-head pair); row unit = one 128-row block (head pairs) or a pair of
 // consecutive blocks of one head.
+template <bool SINK>
 __device__ __forceinline__ WorkItem decode_item(const FwdParams& p, int hu, int r) {
   WorkItem it;
   if (p.pair_heads) {
@@ -212,15 +220,25 @@ __device__ __forceinline__ WorkItem decode_item(const FwdParams& p, int hu, int 
       it.hi[t] = 0;
     }
   }
+  it.ns = SINK ? min(p.sink_tiles, it.lo_u) : 0;
   return it;
 }
 
+// Does a query tile with window tiles lo .. hi work on KV tile j?  (A sink tile lies at or
+// below hi: key 0 is never behind a row's own position.)
+template <bool SINK>
+__device__ __forceinline__ bool tile_active(const FwdParams& p, int lo, int hi, int j) {
+  return j <= hi && (j >= lo || (SINK && j < p.sink_tiles));
+}
+
 // Does KV tile j need element-wise masking for query block m?
+template <bool SINK>
 __device__ __forceinline__ bool tile_is_partial(const FwdParams& p, int m, int j) {
   const int r0 = m * kBlockM + p.key_offset, c0 = j * kBlockN;
   bool partial = (c0 + kBlockN > p.N);
   if (p.mask_kind != kMaskFull) partial |= (c0 + kBlockN - 1 > r0);
-  if (p.mask_kind == kMaskWindow) partial |= (c0 <= r0 + kBlockM - 1 - p.window);
+  if (p.mask_kind == kMaskWindow)
+    partial |= (c0 <= r0 + kBlockM - 1 - p.window) && !(SINK && c0 + kBlockN <= p.sinks);
   return partial;
 }
 
@@ -365,7 +383,7 @@ __device__ __forceinline__ void finish_v_part(uint32_t bar, uint32_t mag, int* e
 }
 
 // Warp 11: the first half of every V tile of this CTA's work, in step order.
-template <int D, int EB>
+template <int D, int EB, bool SINK>
 __device__ __forceinline__ void vconv_role(const FwdParams& p, uint32_t sbase, const Waiter& w, int lane) {
   using L = SmemLayout<D, EB>;
   auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
@@ -373,8 +391,8 @@ __device__ __forceinline__ void vconv_role(const FwdParams& p, uint32_t sbase, c
   Schedule sched(p, blockIdx.x, gridDim.x);
   int hu, r;
   while (sched.next(hu, r)) {
-    const WorkItem it = decode_item(p, hu, r);
-    for (int j = it.lo_u; j <= it.hi_u; ++j, ++v) {
+    const WorkItem it = decode_item<SINK>(p, hu, r);
+    for (int u = it.first_u(); u <= it.hi_u; ++u, ++v) {
       const uint32_t vn = 2 * v + 1, slot = vn % L::kStages;
       const bool got = w.wait(bar(L::kKVFull + slot), (vn / L::kStages) & 1, (kRoleVConv << 8) | (L::kKVFull + slot));
       if (!__all_sync(0xffffffffu, got)) return;
@@ -387,12 +405,12 @@ __device__ __forceinline__ void vconv_role(const FwdParams& p, uint32_t sbase, c
 // ------------------------------------------------------------ roles
 // L2 prefetch of the next work item's Q tiles and of its first two K/V tiles
 // (sched has already moved past the current item).
-template <int D, int EB>
+template <int D, int EB, bool SINK>
 __device__ __forceinline__ void prefetch_next_item(const FwdParams& p, Schedule sched) {
   using L = SmemLayout<D, EB>;
   int hu, r;
   if (!sched.next(hu, r)) return;
-  const WorkItem n = decode_item(p, hu, r);
+  const WorkItem n = decode_item<SINK>(p, hu, r);
 #pragma unroll
   for (int c = 0; c < L::kChunks; ++c) {
     const int x = c * L::kChunkElems;
@@ -401,14 +419,15 @@ __device__ __forceinline__ void prefetch_next_item(const FwdParams& p, Schedule 
       if (n.valid[t]) tma_prefetch_3d(&p.tm_q, x, n.mblk[t] * kBlockM, n.b * p.Hq + n.head[t]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      if (n.lo_u + j > n.hi_u) break;
-      tma_prefetch_3d(&p.tm_k, x, (n.lo_u + j) * kBlockN, n.b * p.Hkv + n.hkv);
-      tma_prefetch_3d(&p.tm_v, x, (n.lo_u + j) * kBlockN, n.b * p.Hkv + n.hkv);
+      if (n.first_u() + j > n.hi_u) break;
+      const int tile = n.tile(n.first_u() + j);
+      tma_prefetch_3d(&p.tm_k, x, tile * kBlockN, n.b * p.Hkv + n.hkv);
+      tma_prefetch_3d(&p.tm_v, x, tile * kBlockN, n.b * p.Hkv + n.hkv);
     }
   }
 }
 
-template <int D, int EB>
+template <int D, int EB, bool SINK>
 __device__ __forceinline__ void producer_role(const FwdParams& p, uint32_t sbase, const Waiter& w) {
   using L = SmemLayout<D, EB>;
   auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
@@ -425,7 +444,7 @@ __device__ __forceinline__ void producer_role(const FwdParams& p, uint32_t sbase
   Schedule sched(p, blockIdx.x, gridDim.x);
   int hu, r;
   while (ok && sched.next(hu, r)) {
-    const WorkItem it = decode_item(p, hu, r);
+    const WorkItem it = decode_item<SINK>(p, hu, r);
     if (p.item_visits) atomicAdd(p.item_visits + static_cast<size_t>(hu) * p.row_units + r, 1u);
     // Q of this item goes into the single Q buffer once the previous item's
     // last S has read it.  The item's first K and V tiles are issued before
@@ -449,9 +468,10 @@ __device__ __forceinline__ void producer_role(const FwdParams& p, uint32_t sbase
     // A few steps before the item ends, start pulling what the next item
     // reads first (its Q tiles and first K/V tiles) into L2, so the next
     // item's loads do not wait on DRAM.
-    const int pf_step = max(it.lo_u, it.hi_u - kPrefetchSteps);
-    for (int j = it.lo_u; j <= it.hi_u && ok; ++j) {
-      if (j == pf_step) prefetch_next_item<D, EB>(p, sched);
+    const int pf_step = max(it.first_u(), it.hi_u - kPrefetchSteps);
+    for (int u = it.first_u(); u <= it.hi_u && ok; ++u) {
+      const int j = it.tile(u);
+      if (u == pf_step) prefetch_next_item<D, EB, SINK>(p, sched);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t slot = kv_n % L::kStages;
@@ -468,7 +488,7 @@ __device__ __forceinline__ void producer_role(const FwdParams& p, uint32_t sbase
           tma_load_3d(sbase + L::kKVOff + slot * L::kTileBytes + c * L::kChunkBytes, map,
                       bar(L::kKVFull + slot), c * L::kChunkElems, j * kBlockN, it.b * p.Hkv + it.hkv, pol_kv);
         ++kv_n;
-        if (j == it.lo_u && kv == 1 && !load_q()) {
+        if (u == it.first_u() && kv == 1 && !load_q()) {
           ok = false;
           break;
         }
@@ -493,7 +513,7 @@ __device__ __forceinline__ void producer_role(const FwdParams& p, uint32_t sbase
 //   S_t  = Q_t K_j^T          (after that P V in issue order, since P aliases S)
 // and releases K_j / V_{j-1} / Q with commits; the other tile's warp does the
 // same, so each ring slot is freed after both warps' reads complete.
-template <int D, int EB, bool F16P>
+template <int D, int EB, bool F16P, bool SINK>
 __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uint32_t tmem, const Waiter& w,
                                          int t) {
   using L = SmemLayout<D, EB>;
@@ -545,7 +565,7 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
   }
   int hu, r;
   while (ok && sched.next(hu, r)) {
-    const WorkItem it = decode_item(p, hu, r);
+    const WorkItem it = decode_item<SINK>(p, hu, r);
     bool more_items = false;  // a step follows this item's last one
     if constexpr (kConvV) {
       Schedule peek = sched;
@@ -600,7 +620,8 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
       return true;
     };
 
-    for (int j = it.lo_u; j <= it.hi_u; ++j) {
+    for (int u = it.first_u(); u <= it.hi_u; ++u) {
+      const int j = it.tile(u);
       const uint32_t kslot = kv_n % L::kStages;
       // K_j is normally resident long before P_t(j-1) is ready; confirming it
       // first lets P V and the next S issue back to back once P arrives.
@@ -613,12 +634,12 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
           ok = false;
           break;
         }
-      } else if (j > it.lo_u && !wait_v_landed(kv_n - 1)) {
+      } else if (u > it.first_u() && !wait_v_landed(kv_n - 1)) {
         ok = false;
         break;
       }
       tc_fence_after_sync();
-      if (valid && j >= lo && j <= hi) {
+      if (valid && tile_active<SINK>(p, lo, hi, j)) {
         const uint64_t kd = k_desc0 + ((kslot * L::kTileBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D * EB / 32; ++kk) {
@@ -639,12 +660,12 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
       // arrival for a load can only come after the load was issued, i.e.
       // after the slot's previous phase completed: no warp ever arrives twice
       // in one phase, even when its own tile is idle and it runs ahead.
-      if (j > it.lo_u) tc_commit_elect(bar(L::kKVEmpty + (kv_n - 1) % L::kStages));  // V_{j-1} read
+      if (u > it.first_u()) tc_commit_elect(bar(L::kKVEmpty + (kv_n - 1) % L::kStages));  // V_{j-1} read
       tc_commit_elect(bar(L::kKVEmpty + kslot));                                   // K_j read
-      if (j == it.hi_u) tc_commit_elect(bar(L::kQEmpty));                          // Q read
+      if (u == it.hi_u) tc_commit_elect(bar(L::kQEmpty));                          // Q read
       if constexpr (kConvV) {
         // This warp's quarter of the next step's V (its P V comes a step later).
-        if ((j < it.hi_u || more_items) && !convert_quarter((kv_n >> 1) + 1)) {
+        if ((u < it.hi_u || more_items) && !convert_quarter((kv_n >> 1) + 1)) {
           ok = false;
           break;
         }
@@ -664,7 +685,7 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
 }
 
 // Eight softmax warps, one thread per query row of their tile.
-template <int D, int EB, bool F16P>
+template <int D, int EB, bool F16P, bool SINK>
 __device__ __forceinline__ void softmax_role(const FwdParams& p, uint32_t sbase, uint32_t tmem,
                                              const Waiter& w, int warp, int lane) {
   using L = SmemLayout<D, EB>;
@@ -686,7 +707,7 @@ __device__ __forceinline__ void softmax_role(const FwdParams& p, uint32_t sbase,
   Schedule sched(p, blockIdx.x, gridDim.x);
   int hu, r;
   while (ok && sched.next(hu, r)) {
-    const WorkItem it = decode_item(p, hu, r);
+    const WorkItem it = decode_item<SINK>(p, hu, r);
     // This warp's tile, picked with selects so the item stays in registers.
     const int mblk = t ? it.mblk[1] : it.mblk[0];
     const int head = t ? it.head[1] : it.head[0];
@@ -701,8 +722,9 @@ __device__ __forceinline__ void softmax_role(const FwdParams& p, uint32_t sbase,
     // the turn token back and forth: the exp loop of one tile runs while
     // the tensor core works on the other tile (the exp unit is the shared
     // bottleneck), whether or not a tile has work at a given step.
-    for (int j = it.lo_u; j <= it.hi_u; ++j) {
-      const bool active = valid && j >= lo && j <= hi;
+    for (int u = it.first_u(); u <= it.hi_u; ++u) {
+      const int j = it.tile(u);
+      const bool active = valid && tile_active<SINK>(p, lo, hi, j);
       float s[128];
       if (active) {
         bool got = w.wait(bar(L::kSFull + t), s_cnt & 1, (kRoleSoftmax << 8) | (L::kSFull + t));
@@ -716,13 +738,14 @@ __device__ __forceinline__ void softmax_role(const FwdParams& p, uint32_t sbase,
         tmem_load_128cols(tS, sr);
 #pragma unroll
         for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(sr[i]);
-        if (tile_is_partial(p, mblk, j)) {
+        if (tile_is_partial<SINK>(p, mblk, j)) {
           const int c0 = j * kBlockN;
           const int hi_i = ((p.mask_kind == kMaskFull) ? p.N - 1 : min(row + p.key_offset, p.N - 1)) - c0;
           const int lo_i = (p.mask_kind == kMaskWindow) ? row + p.key_offset - p.window + 1 - c0 : -1;
+          const int sink_i = SINK ? p.sinks - c0 : 0;  // keys of the tile below it are sinks
 #pragma unroll
           for (int i = 0; i < 128; ++i)
-            if (i > hi_i || i < lo_i) s[i] = -INFINITY;
+            if (i > hi_i || (i < lo_i && !(SINK && i < sink_i))) s[i] = -INFINITY;
         }
       }
       bool need = false;
@@ -810,7 +833,8 @@ __device__ __forceinline__ void softmax_role(const FwdParams& p, uint32_t sbase,
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kTurn + (t ^ 1)));
       } else {
-        if (j > lo && __any_sync(0xffffffffu, need)) {
+        // (With sinks, tile 0 is every query tile's first.)
+        if (j > (SINK ? 0 : lo) && __any_sync(0xffffffffu, need)) {
           // O of this row was last written by the P V of the previous tile; that
           // MMA completed before this S tile did (in-order tcgen05 completion).
 #pragma unroll 1
@@ -899,8 +923,10 @@ __device__ __forceinline__ void softmax_role(const FwdParams& p, uint32_t sbase,
 }
 
 // EB = bytes per input element (2: bf16, 1: E4M3); F16P (bf16 inputs): P and V
-// go to the P V product as fp16 (true) or as bf16 (false).
-template <int D, int EB = 2, bool F16P = true>
+// go to the P V product as fp16 (true) or as bf16 (false); SINK: the sliding
+// window with sinks, as instances of their own so that the other masks' loops
+// carry none of the sinks' index arithmetic.
+template <int D, int EB = 2, bool F16P = true, bool SINK = false>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
   using L = SmemLayout<D, EB>;
   extern __shared__ uint8_t smem_raw[];
@@ -945,17 +971,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 
   if (warp < 8) {
     reg_alloc_raise<kSoftmaxRegs>();
-    softmax_role<D, EB, F16P>(p, sbase, tmem, w, warp, lane);
+    softmax_role<D, EB, F16P, SINK>(p, sbase, tmem, w, warp, lane);
   } else {
     reg_alloc_lower<kOtherRegs>();
   }
   if (warp == kProducerWarp) {
-    if (lane == 0) producer_role<D, EB>(p, sbase, w);
+    if (lane == 0) producer_role<D, EB, SINK>(p, sbase, w);
     __syncwarp();
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-    mma_role<D, EB, F16P>(p, sbase, tmem, w, warp - kMmaWarp);
+    mma_role<D, EB, F16P, SINK>(p, sbase, tmem, w, warp - kMmaWarp);
   } else if (warp == kMmaWarp + 2) {
-    if constexpr (EB == 2 && F16P) vconv_role<D, EB>(p, sbase, w, lane);
+    if constexpr (EB == 2 && F16P) vconv_role<D, EB, SINK>(p, sbase, w, lane);
   }
 
   tc_fence_before_sync();

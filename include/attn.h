@@ -22,6 +22,7 @@
  *   ATTN_MASK_SLIDING_WINDOW  i - window < j <= i (stanleyjacob.dev, section
  *                             "Sliding-window and local attention" and sliding_window_mask);
  *                             a window >= N is exactly causal and is run as causal.
+ *                             With sinks (attn_fwd_options) the first keys stay visible too.
  * Head sharing (GQA/MQA): query head h reads key/value head g(h) = h / (Hq / Hkv)
  * ("Attention Mechanism Variants Beyond Self-Attention", tempatgunting.com, section
  * "Multi-Query and Grouped-Query Attention": repeat_interleave on the head axis).
@@ -116,6 +117,12 @@ typedef struct {
                                key-tile dK/dV kernel; seven matmuls per pair, dq bitwise
                                reproducible, workspace 4 B Hq N bytes, 4-byte aligned);
                                0 = the fused key-tile kernel where Hq == Hkv (default) */
+  int64_t sinks;            /* sliding window (forward, backward, decoding): the first `sinks` keys
+                               stay visible to every row at or behind them, beside the row's window:
+                               key j is visible if j <= i and (j > i - window or j < sinks), with i
+                               the row's position (key_offset added). 0 = none; > 0 is refused with
+                               the other masks, as is < 0. A decoding step looks up the pages that
+                               hold sinks, and none between them and the window */
 } attn_fwd_options;
 
 /* attn_fwd with options (same arguments, same checks); opts may be NULL. */
@@ -277,8 +284,8 @@ int attn_bwd(const void* q, const void* k, const void* v, const void* out, const
              int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t d,
              float scale, int mask_kind, int64_t window, cudaStream_t stream);
 
-/* attn_bwd with options (wait bound and CTA count as for attn_fwd_ex, and
-   bwd_deterministic; the other fields are ignored); opts may be NULL. */
+/* attn_bwd with options (wait bound and CTA count as for attn_fwd_ex, bwd_deterministic and
+   sinks; the other fields are ignored); opts may be NULL. */
 int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, const float* lse,
                 const void* dout, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
                 int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t d,
@@ -350,8 +357,8 @@ int attn_decode(const void* q, const void* k_cache, const void* v_cache, const i
                 int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d,
                 int64_t num_pages, int64_t page_size, int64_t max_pages_per_seq, int64_t num_splits,
                 float scale, int mask_kind, int64_t window, cudaStream_t stream);
-/* attn_decode with options (wait bound and CTA count as for attn_fwd_ex; the other
-   fields are ignored); opts may be NULL. */
+/* attn_decode with options (wait bound and CTA count as for attn_fwd_ex, and sinks; the
+   other fields are ignored); opts may be NULL. */
 int attn_decode_ex(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
                    const int32_t* seq_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
                    int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d,
@@ -512,7 +519,7 @@ int attn_kv_append_debug_error(cudaStream_t stream, int* device_code);
  * Precision: the products take the codes exactly; a bf16 query row is split into two E4M3
  * terms (exact to 2^-18 of the row's largest element); scores, statistics and sums are fp32;
  * softmax weights go to the product with V as sums of three E5M2 numbers (9 significant bits,
- * about bf16's); weights below 2^-28 of a row's largest are dropped there (and only there).
+ * one more than bf16's); weights below 2^-28 of a row's largest are dropped there (and only there).
  * Ownership, checks, overlap rules, bounded waits and errors as attn_decode.
  */
 int attn_decode_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,

@@ -44,21 +44,35 @@ def forward(q, k, v, scale, window, sinks, key_offset=0):
 
 
 def backward(q, k, v, dout, scale, window, sinks):
-    """(dq, dk, dv) of sum(dout * out)."""
+    """((dq, dk, dv), bounds) of sum(dout * out).  The bounds count the roundings of a backward
+    that holds P and dS in bf16 (8 significant bits: spacing 2^-7 of the leading bit, so a
+    rounding is off by up to 2^-8 of the value; dS carries P's and its own), takes D from a bf16
+    out (2^-8 of each |dout out|) and forms scores in fp32 (d + 8 roundings of the sum of |q k|): elementwise
+    limits before the results' own rounding."""
     q, k, v, dout = (np.asarray(t, np.float64) for t in (q, k, v, dout))
     B, Hq, N, d = q.shape
     g = Hq // k.shape[1]
     ok = visible(np.arange(N), np.arange(N), window, sinks)
-    dq, dk, dv = np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)
+    got = [np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)]
+    lim = [np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)]
     for b in range(B):
         for h in range(Hq):
-            p, _ = softmax_rows(scale * (q[b, h] @ k[b, h // g].T), ok)
-            dp = dout[b, h] @ v[b, h // g].T
-            ds = p * (dp - (p * dp).sum(-1, keepdims=True))
-            dq[b, h] = scale * ds @ k[b, h // g]
-            dk[b, h // g] += scale * ds.T @ q[b, h]
-            dv[b, h // g] += p.T @ dout[b, h]
-    return dq, dk, dv
+            qq, kk, vv, do = q[b, h], k[b, h // g], v[b, h // g], dout[b, h]
+            p, _ = softmax_rows(scale * (qq @ kk.T), ok)
+            dp = do @ vv.T
+            D = (p * dp).sum(-1, keepdims=True)
+            ds = p * (dp - D)
+            got[0][b, h] = scale * ds @ kk
+            got[1][b, h // g] += scale * ds.T @ qq
+            got[2][b, h // g] += p.T @ do
+            slip = 2 * scale * (np.abs(qq) @ np.abs(kk).T) * (d + 8) * 2.0 ** -24 + 2.0 ** -18
+            dp_mass = np.abs(do) @ np.abs(vv).T
+            off = (np.abs(do) * (p @ np.abs(vv))).sum(-1, keepdims=True) * 2.0 ** -8
+            e_ds = np.abs(ds) * (2.0 ** -7 + slip) + p * (off + (dp_mass + np.abs(D)) * d * 2.0 ** -24)
+            lim[0][b, h] = scale * e_ds @ np.abs(kk)
+            lim[1][b, h // g] += scale * e_ds.T @ np.abs(qq)
+            lim[2][b, h // g] += (p * (2.0 ** -8 + slip)).T @ np.abs(do)
+    return got, lim
 
 
 def decode(q, k_cache, v_cache, block_table, seq_lens, scale=None, mask="causal", window=None, sinks=0):
