@@ -25,7 +25,7 @@ EXPORTS = ("attn_fwd", "attn_fwd_ex", "attn_status_string", "attn_debug_error", 
            "attn_decode_debug_error", "attn_fwd_fp8", "attn_fwd_fp8_ex", "attn_merge", "attn_fwd_host",
            "attn_fwd_fp8_host", "attn_decode_static", "attn_kv_append", "attn_kv_append_debug_error",
            "attn_decode_kv8", "attn_decode_kv8_workspace_bytes", "attn_decode_kv8_num_splits",
-           "attn_decode_kv8_debug_error")
+           "attn_decode_kv8_debug_error", "attn_bwd_sink_workspace_bytes")
 
 _lib = None
 
@@ -92,6 +92,8 @@ def load_library():
     lib.attn_bwd_ex.restype = ctypes.c_int
     lib.attn_bwd_workspace_bytes.argtypes = [i64, i64, i64]
     lib.attn_bwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_bwd_sink_workspace_bytes.argtypes = [i64] * 7
+    lib.attn_bwd_sink_workspace_bytes.restype = ctypes.c_size_t
     lib.attn_bwd_debug_error.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
     lib.attn_bwd_debug_error.restype = ctypes.c_int
     dec_args = [vp] * 8 + [ctypes.c_size_t] + [i64] * 9 + [ctypes.c_float, ctypes.c_int, i64, vp]
@@ -252,7 +254,7 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ls
     workspace (allocated here when not given) holds the row terms
     D = rowsum(dout * out) and, on the fused path (d = 128, Hq == Hkv), the fp32
     sums of dq: ``attn_bwd_workspace_bytes(B, Hq, N)`` bytes there, B*Hq*N floats
-    otherwise.  ``deterministic`` takes the two-kernel path there too (dq bitwise
+    otherwise, and ``attn_bwd_sink_workspace_bytes`` with ``sinks``.  ``deterministic`` takes the two-kernel path there too (dq bitwise
     reproducible; seven matmuls per pair instead of five).
     """
     lib = load_library()
@@ -277,6 +279,8 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ls
             raise ValueError(f"{name} has the wrong shape")
     fused = d == 128 and Hq == Hkv and not deterministic  # the library's choice of path
     ws_bytes = int(lib.attn_bwd_workspace_bytes(B, Hq, N)) if fused else 4 * B * Hq * N
+    if sinks and mask == "sliding_window" and window is not None:
+        ws_bytes = int(lib.attn_bwd_sink_workspace_bytes(B, Hq, Hkv, N, d, int(window), int(sinks)))
     if workspace is None:
         workspace = torch.empty(ws_bytes // 4, dtype=torch.float32, device=q.device)
     if not (workspace.is_cuda and workspace.is_contiguous()):

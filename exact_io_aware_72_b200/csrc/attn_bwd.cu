@@ -56,10 +56,16 @@ struct BwdDevice {
 std::mutex g_bwd_mutex;
 BwdDevice g_bwd_dev[kMaxDevices];
 
-template <int D, int KIND>
+template <int D, int KIND, bool SINK>
 cudaError_t set_smem() {
-  return cudaFuncSetAttribute(attn_bwd_kernel<D, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(attn_bwd_kernel<D, KIND, SINK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               BwdSmem<D>::kAlloc);
+}
+template <bool SINK>
+bool set_smem_all() {
+  return set_smem<128, kBKernelFused, SINK>() == cudaSuccess && set_smem<64, kBKernelDkdvFull, SINK>() == cudaSuccess &&
+         set_smem<128, kBKernelDkdvFull, SINK>() == cudaSuccess && set_smem<64, kBKernelDqFull, SINK>() == cudaSuccess &&
+         set_smem<128, kBKernelDqFull, SINK>() == cudaSuccess;
 }
 
 int bwd_device_setup(BwdDevice& out) {
@@ -80,9 +86,7 @@ int bwd_device_setup(BwdDevice& out) {
       void* addr = nullptr;
       if (cudaGetSymbolAddress(&addr, g_attn_bwd_error) != cudaSuccess) return ATTN_ERR_CUDA;
       info.err_word = static_cast<int*>(addr);
-      if (set_smem<128, kBKernelFused>() != cudaSuccess || set_smem<64, kBKernelDkdvFull>() != cudaSuccess ||
-          set_smem<128, kBKernelDkdvFull>() != cudaSuccess || set_smem<64, kBKernelDqFull>() != cudaSuccess ||
-          set_smem<128, kBKernelDqFull>() != cudaSuccess)
+      if (!set_smem_all<false>() || !set_smem_all<true>())
         return ATTN_ERR_CUDA;
     }
     info.probed = true;
@@ -111,14 +115,18 @@ bool sizes_ok(int64_t B, int64_t Hq, int64_t Hkv, int64_t N) {
          B * Hq <= (int64_t(1) << 30) && B * Hq * ((N + kTile - 1) / kTile) <= 0x7fffffff;
 }
 
-template <int D, int KIND>
-cudaError_t launch_bwd(const BwdParams& p, int grid, cudaStream_t stream) {
+template <int D, int KIND, bool SINK>
+cudaError_t launch_instance(const BwdParams& p, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(bwd_threads<KIND>());
   cfg.dynamicSmemBytes = BwdSmem<D>::kAlloc;
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, attn_bwd_kernel<D, KIND>, p);
+  return cudaLaunchKernelEx(&cfg, attn_bwd_kernel<D, KIND, SINK>, p);
+}
+template <int D, int KIND>
+cudaError_t launch_bwd(const BwdParams& p, int grid, cudaStream_t stream) {
+  return p.sinks ? launch_instance<D, KIND, true>(p, grid, stream) : launch_instance<D, KIND, false>(p, grid, stream);
 }
 
 }  // namespace
@@ -136,12 +144,40 @@ size_t bwd_workspace_bytes(int64_t B, int64_t Hq, int64_t N, int64_t acc_d) {
   if (acc_d == 0) return delta;
   return ((delta + 255) & ~size_t(255)) + rows * static_cast<size_t>(acc_d) * sizeof(float);
 }
+
+// Sinks: how the key tiles that hold sinks are cut, and the bytes of their partial sums.
+struct SinkPlan {
+  int64_t sinks = 0, tiles = 0, parts = 0;
+  size_t bytes = 0;
+};
+SinkPlan sink_plan(int64_t B, int64_t Hkv, int64_t N, int64_t d, int64_t window, int64_t sinks) {
+  SinkPlan s;
+  s.sinks = std::min(sinks, N);
+  if (s.sinks < 1 || window >= N - s.sinks) return SinkPlan{};  // every earlier key is visible: plain causal
+  const int64_t blk = (N + kTile - 1) / kTile;
+  s.tiles = (s.sinks + kTile - 1) / kTile;
+  // A part is about as long as an ordinary key tile's window of query tiles, at least eight
+  // tiles (a part's 128 x d fp32 sums take about as long to write as one step).
+  const int64_t len = std::max<int64_t>(8, std::min(blk, (window + kTile - 1) / kTile + 1));
+  s.parts = std::max<int64_t>(1, std::min((blk + len - 1) / len, blk - s.tiles + 1));
+  if (s.parts > 1) s.bytes = static_cast<size_t>(B * Hkv) * s.tiles * s.parts * 2 * kTile * d * sizeof(float);
+  return s;
+}
 }  // namespace
 
 extern "C" {
 
 size_t attn_bwd_workspace_bytes(int64_t B, int64_t Hq, int64_t N) {
   return bwd_workspace_bytes(B, Hq, N, 128);  // covers every supported head dimension
+}
+
+size_t attn_bwd_sink_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t d, int64_t window,
+                                     int64_t sinks) {
+  if (!sizes_ok(B, Hq, Hkv, N) || (d != 64 && d != 128) || window < 1 || sinks < 0) return 0;
+  const size_t base = bwd_workspace_bytes(B, Hq, N, 128);
+  const SinkPlan s = sink_plan(B, Hkv, N, d, window, sinks);
+  if (base == 0 || s.bytes > (size_t(1) << 61)) return 0;
+  return ((base + 255) & ~size_t(255)) + s.bytes;
 }
 
 int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout,
@@ -163,7 +199,14 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
   // tile's dQ partial sums go to every query head of its group, whose fp32 accumulators
   // (and Q, dO) then outgrow L2; there the two-kernel path measured faster.
   const bool fused = (d == 128) && Hq == Hkv && !(opts && opts->bwd_deterministic);
-  const size_t ws = bwd_workspace_bytes(B, Hq, N, fused ? 128 : 0);
+  size_t ws = bwd_workspace_bytes(B, Hq, N, fused ? 128 : 0);
+  const SinkPlan sink = sinks ? sink_plan(B, Hkv, N, d, window, sinks) : SinkPlan{};
+  const size_t part_off = (ws + 255) & ~size_t(255);
+  // dK, dV: one key tile per item, or one part of a sink tile's queries.
+  const int64_t blk = (N + kTile - 1) / kTile;
+  const int64_t key_items = B * Hkv * (blk + sink.tiles * (sink.parts - 1));
+  if (key_items > 0x7fffffff) return ATTN_ERR_INVALID_ARG;
+  if (ws != 0 && sink.bytes) ws = part_off + sink.bytes;
   if (ws == 0 || workspace_bytes < ws) return ATTN_ERR_INVALID_ARG;
   const size_t q_bytes = static_cast<size_t>(B * Hq * N * d) * 2;
   const size_t kv_bytes = static_cast<size_t>(B * Hkv * N * d) * 2;
@@ -181,7 +224,7 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
   auto mis16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; };
   if (mis16(q) || mis16(k) || mis16(v) || mis16(out) || mis16(dout) || mis16(dq) || mis16(dk) || mis16(dv) ||
       (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 ||
-      (reinterpret_cast<uintptr_t>(workspace) & (fused ? 15u : 3u)) != 0)
+      (reinterpret_cast<uintptr_t>(workspace) & (fused || sink.bytes ? 15u : 3u)) != 0)
     return ATTN_ERR_MISALIGNED;
 
   BwdDevice info;
@@ -213,7 +256,10 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
   p.group = static_cast<int>(Hq / Hkv);
   p.mask_kind = kind;
   p.window = static_cast<int>(kind == ATTN_MASK_SLIDING_WINDOW ? w : N);
-  p.sinks = static_cast<int>(kind == ATTN_MASK_SLIDING_WINDOW ? sinks : 0);
+  p.sinks = static_cast<int>(sink.sinks);  // 0 where the mask is causal
+  p.sink_tiles = static_cast<int>(sink.tiles);
+  p.sink_parts = static_cast<int>(sink.parts);
+  p.part = sink.bytes ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_off) : nullptr;
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.num_blk = static_cast<int>((N + kTile - 1) / kTile);
@@ -236,6 +282,13 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
   int sms = info.sm_count;
   if (opts && opts->grid_ctas > 0) sms = opts->grid_ctas;
   cudaError_t e;
+  auto reduce_sinks = [&]() -> cudaError_t {
+    if (!p.part) return cudaSuccess;
+    const unsigned tiles = static_cast<unsigned>(B * Hkv * sink.tiles);
+    if (d == 128) attn_bwd_sink_reduce_kernel<128><<<dim3(2 * tiles, kTile * 128 / 4 / 256), 256, 0, stream>>>(p);
+    else attn_bwd_sink_reduce_kernel<64><<<dim3(2 * tiles, kTile * 64 / 4 / 256), 256, 0, stream>>>(p);
+    return cudaGetLastError();
+  };
   if (fused) {
     // Fused: dK, dV and the fp32 dQ sums in one key-tile kernel, then dQ to bf16.
     const size_t acc_off = (static_cast<size_t>(rows) * sizeof(float) + 255) & ~size_t(255);
@@ -243,9 +296,10 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
     const size_t acc_bytes = static_cast<size_t>(rows) * 128 * sizeof(float);
     if (cudaMemsetAsync(acc, 0, acc_bytes, stream) != cudaSuccess) return ATTN_ERR_CUDA;
     p.dq_acc = acc;
-    p.num_items = static_cast<int>(B * Hkv * p.num_blk);  // one key tile per item
+    p.num_items = static_cast<int>(key_items);
     const int grid = static_cast<int>(std::min<int64_t>(sms, p.num_items));
     if (launch_bwd<128, kBKernelFused>(p, grid, stream) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (reduce_sinks() != cudaSuccess) return ATTN_ERR_CUDA;
     const int64_t groups8 = rows * 128 / 8;
     const unsigned cblocks = static_cast<unsigned>(std::min<int64_t>((groups8 + 255) / 256, int64_t(info.sm_count) * 16));
     attn_bwd_dq_convert_kernel<<<cblocks, 256, 0, stream>>>(acc, static_cast<__nv_bfloat16*>(dq), scale, groups8);
@@ -255,10 +309,11 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
   int grid = static_cast<int>(std::min<int64_t>(sms, p.num_items));
   e = (d == 128) ? launch_bwd<128, kBKernelDqFull>(p, grid, stream) : launch_bwd<64, kBKernelDqFull>(p, grid, stream);
   if (e != cudaSuccess) return ATTN_ERR_CUDA;
-  p.num_items = static_cast<int>(B * Hkv * p.num_blk);  // dK, dV: one key tile per item
+  p.num_items = static_cast<int>(key_items);
   grid = static_cast<int>(std::min<int64_t>(sms, p.num_items));
   e = (d == 128) ? launch_bwd<128, kBKernelDkdvFull>(p, grid, stream)
                  : launch_bwd<64, kBKernelDkdvFull>(p, grid, stream);
+  if (e == cudaSuccess) e = reduce_sinks();
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

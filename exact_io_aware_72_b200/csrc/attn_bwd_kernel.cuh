@@ -74,7 +74,10 @@ struct BwdParams {
   int* err;           // device error word (shared with the forward)
   int B, Hq, Hkv, N, group;
   int mask_kind, window;
-  int sinks;          // window mask: keys below it stay visible to every later query
+  int sinks;          // SINK kernels (window mask): keys below it stay visible to every later query
+  int sink_tiles;     // ceil(sinks / 128)
+  int sink_parts;     // items that a sink tile's queries are cut into (see DkvItem)
+  float* part;        // sink_parts > 1: [B*Hkv][sink_tiles][sink_parts][dV, dK][128, d] fp32 sums
   float scale;        // softmax scale (dQ, dK are scaled by it)
   float scale_log2;   // scale * log2(e)
   int num_blk;        // ceil(N / 128)
@@ -105,17 +108,17 @@ __device__ __forceinline__ void query_tiles_of_key_tile(const BwdParams& p, int 
   } else {
     lo = c0 / kTile;  // query i sees key j only if j <= i
     // window: key j is seen by queries i with j <= i <= j + w - 1
-    // (a sink by all from j on)
-    hi = (p.mask_kind == kBMaskWindow && c0 >= p.sinks) ? min(p.num_blk - 1, (c1 + p.window - 1) / kTile)
-                                                        : p.num_blk - 1;
+    hi = (p.mask_kind == kBMaskWindow) ? min(p.num_blk - 1, (c1 + p.window - 1) / kTile) : p.num_blk - 1;
   }
 }
 // Does the (query tile m, key tile n) block need element masks?
+template <bool SINK>
 __device__ __forceinline__ bool block_is_partial(const BwdParams& p, int m, int n) {
   const int r0 = m * kTile, c0 = n * kTile;
   bool partial = (c0 + kTile > p.N) || (r0 + kTile > p.N);
   if (p.mask_kind != kBMaskFull) partial |= (c0 + kTile - 1 > r0);
-  if (p.mask_kind == kBMaskWindow) partial |= (c0 <= r0 + kTile - 1 - p.window) && c0 + kTile > p.sinks;
+  if (p.mask_kind == kBMaskWindow)
+    partial |= (c0 <= r0 + kTile - 1 - p.window) && !(SINK && c0 + kTile <= p.sinks);
   return partial;
 }
 
@@ -190,6 +193,34 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// P between S and dP in the full-tile kernels: two values in a word.  The SINK kernels hold
+// fp16 (11 significant bits: P is at most 1) so that dS carries its own bf16 rounding alone;
+// the others hold the bf16 that the dV product takes, which adds as much again to dS (dq and
+// dk off by 2.9e-3 of their norm instead of 2.4e-3).
+template <bool SINK>
+__device__ __forceinline__ uint32_t hold_p(float lo, float hi) {
+  return SINK ? pack_f16x2(lo, hi) : bf16x2_rn(lo, hi);
+}
+__device__ __forceinline__ float2 f16x2_values(uint32_t w) {
+  float2 v;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+      : "=f"(v.x), "=f"(v.y)
+      : "r"(w));
+  return v;
+}
+template <bool SINK>
+__device__ __forceinline__ uint64_t held_p(uint32_t w) {
+  if constexpr (SINK) {
+    const float2 v = f16x2_values(w);
+    return f32x2_pack(v.x, v.y);
+  }
+  return f32x2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
+  const float2 v = f16x2_values(w);
+  return bf16x2_rn(v.x, v.y);
 }
 
 // ------------------------------------------------------------------ delta
@@ -305,12 +336,26 @@ __device__ __forceinline__ void store_acc_row(uint32_t tacc, float mul, __nv_bfl
   }
 }
 
+// The same row unscaled in fp32.
+template <int D>
+__device__ __forceinline__ void store_acc_row_f32(uint32_t tacc, float* dst_row) {
+#pragma unroll 1
+  for (int cc = 0; cc < D / 32; ++cc) {
+    uint32_t o[32];
+    tmem_load_32cols(tacc + cc * 32, o);
+    uint4* dst = reinterpret_cast<uint4*>(dst_row) + cc * 8;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) dst[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+  }
+}
+
 // ------------------------------------------------------------------ query-tile work items and loader
 struct DqItem {
   int b, hq, hkv, m, lo, hi;
   int ns;  // sink tiles before lo: the item's steps are u = lo - ns .. hi
   __device__ __forceinline__ int tile(int u) const { return u < lo ? u - (lo - ns) : u; }
 };
+template <bool SINK>
 __device__ __forceinline__ DqItem dq_item(const BwdParams& p, int i) {
   DqItem it;
   const int bh = i / p.num_blk;
@@ -319,11 +364,11 @@ __device__ __forceinline__ DqItem dq_item(const BwdParams& p, int i) {
   it.hq = bh - it.b * p.Hq;
   it.hkv = it.hq / p.group;
   key_tiles_of_query_tile(p, it.m, it.lo, it.hi);
-  it.ns = min((p.sinks + kTile - 1) / kTile, it.lo);
+  it.ns = SINK ? min(p.sink_tiles, it.lo) : 0;
   return it;
 }
 
-template <int D>
+template <int D, bool SINK>
 __device__ __forceinline__ void dq_loader(const BwdParams& p, uint32_t sbase, const BwdWaiter& w) {
   using L = BwdSmem<D>;
   auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
@@ -334,7 +379,7 @@ __device__ __forceinline__ void dq_loader(const BwdParams& p, uint32_t sbase, co
   int items = 0;
   bool ok = true;
   for (int i = blockIdx.x; ok && i < p.num_items; i += gridDim.x, ++items) {
-    const DqItem it = dq_item(p, i);
+    const DqItem it = dq_item<SINK>(p, i);
     if (items > 0 && !w.wait(bar(L::kFixEmpty), (items - 1) & 1, (kBKernelDq << 12) | (kBRoleLoader << 8) | L::kFixEmpty)) {
       ok = false;
       break;
@@ -380,11 +425,42 @@ __device__ __forceinline__ void dq_loader(const BwdParams& p, uint32_t sbase, co
 }
 
 // ------------------------------------------------------------------ key-tile work items and loader; the fused kernel (64-query halves)
+// With sinks a key tile that holds some is seen by every later query tile, not by its
+// window's alone: up to N / 128 of them against a handful, which left one CTA working long
+// after the others (2.2 times the whole time without sinks at N = 16384, window 1024).  So
+// its query tiles are cut into sink_parts items of about a window's length, numbered first;
+// each writes its fp32 sums to the workspace, and attn_bwd_sink_reduce_kernel adds them in a
+// fixed order.
 struct DkvItem {
   int b, hkv, n, qlo, qhi, steps;  // steps = group * (qhi - qlo + 1)
+  int part;                        // SINK kernels: index of the item's partial sums, -1 if none
 };
+template <bool SINK>
 __device__ __forceinline__ DkvItem dkv_item(const BwdParams& p, int i) {
   DkvItem it;
+  it.part = -1;
+  if constexpr (SINK) {
+    const int per_head = p.sink_tiles * p.sink_parts, sink_items = p.B * p.Hkv * per_head;
+    int bk;
+    if (i < sink_items) {
+      bk = i / per_head;
+      const int rest = i - bk * per_head, c = rest % p.sink_parts;
+      it.n = rest / p.sink_parts;
+      const int len = p.num_blk - it.n;  // >= sink_parts, so no item is empty
+      it.qlo = it.n + static_cast<int>(static_cast<int64_t>(len) * c / p.sink_parts);
+      it.qhi = it.n + static_cast<int>(static_cast<int64_t>(len) * (c + 1) / p.sink_parts) - 1;
+      if (p.sink_parts > 1) it.part = i;
+    } else {
+      const int near = p.num_blk - p.sink_tiles;
+      bk = (i - sink_items) / near;
+      it.n = p.sink_tiles + (i - sink_items) - bk * near;
+      query_tiles_of_key_tile(p, it.n, it.qlo, it.qhi);
+    }
+    it.b = bk / p.Hkv;
+    it.hkv = bk - it.b * p.Hkv;
+    it.steps = p.group * (it.qhi - it.qlo + 1);
+    return it;
+  }
   const int bk = i / p.num_blk;
   it.n = i - bk * p.num_blk;  // under a causal mask the first key tiles see the most queries
   it.b = bk / p.Hkv;
@@ -404,7 +480,7 @@ __device__ __forceinline__ void dkv_step(const BwdParams& p, const DkvItem& it, 
 // kSplit (the full-tile key-tile kernel): a slot's Q and dO tiles land and are
 // released through their own barriers, so Q can be refilled as soon as the
 // products that read it are done.
-template <int D, bool kSplit>
+template <int D, bool kSplit, bool SINK>
 __device__ __forceinline__ void dkv_loader(const BwdParams& p, uint32_t sbase, const BwdWaiter& w) {
   using L = BwdSmem<D>;
   auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
@@ -416,7 +492,7 @@ __device__ __forceinline__ void dkv_loader(const BwdParams& p, uint32_t sbase, c
   int items = 0;
   bool ok = true;
   for (int i = blockIdx.x; ok && i < p.num_items; i += gridDim.x, ++items) {
-    const DkvItem it = dkv_item(p, i);
+    const DkvItem it = dkv_item<SINK>(p, i);
     if (items > 0 && !w.wait(bar(L::kFixEmpty), (items - 1) & 1, code | L::kFixEmpty)) {
       ok = false;
       break;
@@ -470,7 +546,7 @@ __device__ __forceinline__ void dkv_loader(const BwdParams& p, uint32_t sbase, c
   if (fix_issued > 0) w.drain(bar(L::kFixFull), (fix_issued - 1) & 1, code | L::kFixFull);
 }
 
-template <int D>
+template <int D, bool SINK>
 __device__ __forceinline__ void dkv_mma(const BwdParams& p, uint32_t sbase, uint32_t tmem, const BwdWaiter& w) {
   using L = BwdSmem<D>;
   static_assert(D == 128, "the fused dQ^T product has M = d = 128");
@@ -518,7 +594,7 @@ __device__ __forceinline__ void dkv_mma(const BwdParams& p, uint32_t sbase, uint
     return true;
   };
   for (int i = blockIdx.x; ok && i < p.num_items; i += gridDim.x, ++items) {
-    const DkvItem it = dkv_item(p, i);
+    const DkvItem it = dkv_item<SINK>(p, i);
     if (!w.wait_warp(bar(L::kFixFull), items & 1, code | L::kFixFull)) break;
     tc_fence_after_sync();
     uint32_t prev_slot = 0;
@@ -569,7 +645,7 @@ __device__ __forceinline__ void dkv_mma(const BwdParams& p, uint32_t sbase, uint
   }
 }
 
-template <int D>
+template <int D, bool SINK>
 __device__ __forceinline__ void dkv_elem(const BwdParams& p, uint32_t sbase, uint32_t tmem, const BwdWaiter& w,
                                          int warp, int lane) {
   using L = BwdSmem<D>;
@@ -603,7 +679,7 @@ __device__ __forceinline__ void dkv_elem(const BwdParams& p, uint32_t sbase, uin
   bool fetched = false;  // the next step's vectors are already on their way
   int items = 0;
   for (int i = blockIdx.x; i < p.num_items; i += gridDim.x, ++items) {
-    const DkvItem it = dkv_item(p, i);
+    const DkvItem it = dkv_item<SINK>(p, i);
     const int key = it.n * kTile + r;
     bool ok = true;
     for (int s = 0; s < it.steps && ok; ++s, ++s_cnt) {
@@ -630,14 +706,14 @@ __device__ __forceinline__ void dkv_elem(const BwdParams& p, uint32_t sbase, uin
           fetch_vectors(it.b, hq2, m2, buf ^ 1);
           fetched = true;
         } else if (i + static_cast<int>(gridDim.x) < p.num_items) {
-          const DkvItem nx = dkv_item(p, i + gridDim.x);
+          const DkvItem nx = dkv_item<SINK>(p, i + gridDim.x);
           int hq2, m2;
           dkv_step(p, nx, 0, hq2, m2);
           fetch_vectors(nx.b, hq2, m2, buf ^ 1);
           fetched = true;
         }
       }
-      const bool partial = block_is_partial(p, m, it.n);
+      const bool partial = block_is_partial<SINK>(p, m, it.n);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         if (!w.wait_warp(bar(L::kSFull + h), s_cnt & 1, code | (L::kSFull + h))) {
@@ -655,7 +731,7 @@ __device__ __forceinline__ void dkv_elem(const BwdParams& p, uint32_t sbase, uin
         // (applied on partial tiles, where masked scores become -inf).
         const int q0 = m * kTile + h * kHalf;
         const int hi_c =
-            (key < p.N) ? min(p.N - 1, p.mask_kind == kBMaskWindow && key >= p.sinks ? key + p.window - 1 : p.N - 1) - q0 : -1;
+            (key < p.N) ? min(p.N - 1, p.mask_kind == kBMaskWindow && !(SINK && key < p.sinks) ? key + p.window - 1 : p.N - 1) - q0 : -1;
         const int lo_c = (p.mask_kind == kBMaskFull) ? 0 : key - q0;
         const uint32_t t_s = tmem + lane_bits + L::col_s(h), t_p = tmem + lane_bits + L::col_p(h);
         uint32_t pk[2][16], dk[2][16];
@@ -716,8 +792,14 @@ __device__ __forceinline__ void dkv_elem(const BwdParams& p, uint32_t sbase, uin
     tc_fence_after_sync();
     const bool key_ok = key < p.N;
     const size_t krow = (static_cast<size_t>(it.b) * p.Hkv + it.hkv) * p.N + (key_ok ? key : 0);
-    store_acc_row<D>(t_dv, 1.f, p.dv + krow * D, key_ok);
-    store_acc_row<D>(t_dk, p.scale, p.dk + krow * D, key_ok);
+    if (SINK && it.part >= 0) {
+      float* dst = p.part + (static_cast<size_t>(it.part) * 2 * kTile + r) * D;
+      store_acc_row_f32<D>(t_dv, dst);
+      store_acc_row_f32<D>(t_dk, dst + kTile * D);
+    } else {
+      store_acc_row<D>(t_dv, 1.f, p.dv + krow * D, key_ok);
+      store_acc_row<D>(t_dk, p.scale, p.dk + krow * D, key_ok);
+    }
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(L::kAccFree));
@@ -735,7 +817,7 @@ __device__ __forceinline__ void dkv_elem(const BwdParams& p, uint32_t sbase, uin
 //   dP(g) -> Y       behind it,
 // so the exponentials of tile g run while the tensor core does dQ of tile g-1
 // and dP of tile g.  P is kept as bf16 until dP arrives.
-template <int D>
+template <int D, bool SINK>
 __device__ __forceinline__ void dqf_mma(const BwdParams& p, uint32_t sbase, uint32_t tmem, const BwdWaiter& w) {
   using L = BwdSmem<D>;
   auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
@@ -771,7 +853,7 @@ __device__ __forceinline__ void dqf_mma(const BwdParams& p, uint32_t sbase, uint
     return true;
   };
   for (int i = blockIdx.x; ok && i < p.num_items; i += gridDim.x, ++items) {
-    const DqItem it = dq_item(p, i);
+    const DqItem it = dq_item<SINK>(p, i);
     if (!w.wait_warp(bar(L::kFixFull), items & 1, code | L::kFixFull)) break;
     tc_fence_after_sync();
     for (int u = it.lo - it.ns; u <= it.hi; ++u, ++g) {
@@ -810,7 +892,7 @@ __device__ __forceinline__ void dqf_mma(const BwdParams& p, uint32_t sbase, uint
   if (ok && pend) issue_b();
 }
 
-template <int D>
+template <int D, bool SINK>
 __device__ __forceinline__ void dqf_elem(const BwdParams& p, uint32_t sbase, uint32_t tmem, const BwdWaiter& w,
                                          int warp, int lane) {
   using L = BwdSmem<D>;
@@ -825,7 +907,7 @@ __device__ __forceinline__ void dqf_elem(const BwdParams& p, uint32_t sbase, uin
   uint32_t g = 0;
   int items = 0;
   for (int i = blockIdx.x; i < p.num_items; i += gridDim.x, ++items) {
-    const DqItem it = dq_item(p, i);
+    const DqItem it = dq_item<SINK>(p, i);
     const int row = it.m * kTile + r;
     const bool row_ok = row < p.N;
     const size_t bhrow = (static_cast<size_t>(it.b) * p.Hq + it.hq) * p.N + (row_ok ? row : 0);
@@ -845,23 +927,32 @@ __device__ __forceinline__ void dqf_elem(const BwdParams& p, uint32_t sbase, uin
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kXFree));
-      if (block_is_partial(p, it.m, j)) {
+      if (block_is_partial<SINK>(p, it.m, j)) {
         // Visible key columns of this row: lo_c <= c <= hi_c.
         const int j0 = j * kTile;
         const int hi_c = row_ok ? min(p.N - 1, p.mask_kind == kBMaskFull ? p.N - 1 : row) - j0 : -1;
         const int lo_c = (p.mask_kind == kBMaskWindow) ? row - p.window + 1 - j0 : 0;
-        const int sink_c = p.sinks - j0;  // columns below it are sinks
+        if constexpr (SINK) {
 #pragma unroll
-        for (int c = 0; c < kTile; ++c)
-          if (c > hi_c || (c < lo_c && c >= sink_c)) sv[c] = 0xff800000u;  // -inf
+          for (int w32 = 0; w32 < 4; ++w32) {
+            const uint32_t seen = seen_bits(32 * w32, lo_c, hi_c + 1, p.sinks - j0);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(seen & (1u << c))) sv[32 * w32 + c] = 0xff800000u;  // -inf
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            if (c > hi_c || c < lo_c) sv[c] = 0xff800000u;  // -inf
+        }
       }
-      uint32_t pk[kTile / 2];  // P, bf16 pairs of keys
+      uint32_t pk[kTile / 2];  // P, pairs of keys (SINK: fp16, see hold_p)
 #pragma unroll
       for (int c = 0; c < kTile; c += 2) {
         float x0, x1;
         f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), c2x2, nlse2x2), x0,
                      x1);
-        pk[c >> 1] = bf16x2_rn(bexp2(x0), bexp2(x1));
+        pk[c >> 1] = hold_p<SINK>(bexp2(x0), bexp2(x1));
       }
       if (!w.wait_warp(bar(kDpFull), g & 1, code | kDpFull)) {
         ok = false;
@@ -877,7 +968,7 @@ __device__ __forceinline__ void dqf_elem(const BwdParams& p, uint32_t sbase, uin
         for (int e = 0; e < 32; e += 2) {
           const uint32_t pw = pk[(chunk * 32 + e) >> 1];
           float d0, d1;
-          f32x2_unpack(f32x2_mul(f32x2_pack(__uint_as_float(pw << 16), __uint_as_float(pw & 0xffff0000u)),
+          f32x2_unpack(f32x2_mul(held_p<SINK>(pw),
                                  f32x2_add(f32x2_pack(__uint_as_float(pv[e]), __uint_as_float(pv[e + 1])), ndlt2)),
                        d0, d1);
           ds[(chunk * 32 + e) >> 1] = bf16x2_rn(d0, d1);
@@ -914,7 +1005,7 @@ __device__ __forceinline__ void dqf_elem(const BwdParams& p, uint32_t sbase, uin
 // so the exponentials of step g run while the tensor core does dV, dK of step g-1
 // and dP^T of step g.  P is kept as bf16 until dP arrives; dS = P (dP - D) is
 // formed from that bf16 P.
-template <int D>
+template <int D, bool SINK>
 __device__ __forceinline__ void dkvf_mma(const BwdParams& p, uint32_t sbase, uint32_t tmem, const BwdWaiter& w) {
   using L = BwdSmem<D>;
   auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
@@ -958,7 +1049,7 @@ __device__ __forceinline__ void dkvf_mma(const BwdParams& p, uint32_t sbase, uin
     return true;
   };
   for (int i = blockIdx.x; ok && i < p.num_items; i += gridDim.x, ++items) {
-    const DkvItem it = dkv_item(p, i);
+    const DkvItem it = dkv_item<SINK>(p, i);
     if (!w.wait_warp(bar(L::kFixFull), items & 1, code | L::kFixFull)) break;
     tc_fence_after_sync();
     for (int s = 0; s < it.steps; ++s, ++g) {
@@ -1003,7 +1094,7 @@ __device__ __forceinline__ void dkvf_mma(const BwdParams& p, uint32_t sbase, uin
   if (ok && pend) issue_b();  // the last step's dV, dK
 }
 
-template <int D>
+template <int D, bool SINK>
 __device__ __forceinline__ void dkvf_elem(const BwdParams& p, uint32_t sbase, uint32_t tmem, const BwdWaiter& w,
                                           int warp, int lane) {
   using L = BwdSmem<D>;
@@ -1037,7 +1128,7 @@ __device__ __forceinline__ void dkvf_elem(const BwdParams& p, uint32_t sbase, ui
   bool fetched = false;
   int items = 0;
   for (int i = blockIdx.x; i < p.num_items; i += gridDim.x, ++items) {
-    const DkvItem it = dkv_item(p, i);
+    const DkvItem it = dkv_item<SINK>(p, i);
     const int key = it.n * kTile + r;
     bool ok = true;
     for (int s = 0; s < it.steps && ok; ++s, ++g) {
@@ -1063,7 +1154,7 @@ __device__ __forceinline__ void dkvf_elem(const BwdParams& p, uint32_t sbase, ui
           fetch_vectors(it.b, hq2, m2, buf ^ 1);
           fetched = true;
         } else if (i + static_cast<int>(gridDim.x) < p.num_items) {
-          const DkvItem nx = dkv_item(p, i + gridDim.x);
+          const DkvItem nx = dkv_item<SINK>(p, i + gridDim.x);
           int hq2, m2;
           dkv_step(p, nx, 0, hq2, m2);
           fetch_vectors(nx.b, hq2, m2, buf ^ 1);
@@ -1081,11 +1172,11 @@ __device__ __forceinline__ void dkvf_elem(const BwdParams& p, uint32_t sbase, ui
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kXFree));
-      if (block_is_partial(p, m, it.n)) {
+      if (block_is_partial<SINK>(p, m, it.n)) {
         // Query columns that see this key: lo_c <= c <= hi_c.
         const int q0 = m * kTile;
         const int hi_c =
-            (key < p.N) ? min(p.N - 1, p.mask_kind == kBMaskWindow && key >= p.sinks ? key + p.window - 1 : p.N - 1) - q0 : -1;
+            (key < p.N) ? min(p.N - 1, p.mask_kind == kBMaskWindow && !(SINK && key < p.sinks) ? key + p.window - 1 : p.N - 1) - q0 : -1;
         const int lo_c = (p.mask_kind == kBMaskFull) ? 0 : key - q0;
 #pragma unroll
         for (int c = 0; c < kTile; ++c)
@@ -1100,7 +1191,7 @@ __device__ __forceinline__ void dkvf_elem(const BwdParams& p, uint32_t sbase, ui
         f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), c2x2,
                                f32x2_pack(nl.x, nl.y)),
                      x0, x1);
-        pk[c >> 1] = bf16x2_rn(bexp2(x0), bexp2(x1));
+        pk[c >> 1] = hold_p<SINK>(bexp2(x0), bexp2(x1));
       }
       // dS^T = P (dP - D) once dP^T is in Y, 32 queries at a time; P^T and dS^T go
       // over Y only where dP^T has been read.
@@ -1120,13 +1211,23 @@ __device__ __forceinline__ void dkvf_elem(const BwdParams& p, uint32_t sbase, ui
           const float2 nd = *reinterpret_cast<const float2*>(s_dlt + c);
           const uint32_t pw = pk[c >> 1];
           float d0, d1;
-          f32x2_unpack(f32x2_mul(f32x2_pack(__uint_as_float(pw << 16), __uint_as_float(pw & 0xffff0000u)),
+          f32x2_unpack(f32x2_mul(held_p<SINK>(pw),
                                  f32x2_add(f32x2_pack(__uint_as_float(pv[e]), __uint_as_float(pv[e + 1])),
                                            f32x2_pack(nd.x, nd.y))),
                        d0, d1);
           dk[c >> 1] = bf16x2_rn(d0, d1);
         }
-        if (chunk == 1) tmem_store_32cols(tY, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));  // Y[0, 32) read
+        if (chunk == 1) {  // Y[0, 32) read
+          if constexpr (SINK) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) pk[c] = f16x2_to_bf16x2(pk[c]);
+          }
+          tmem_store_32cols(tY, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+        }
+      }
+      if constexpr (SINK) {
+#pragma unroll
+        for (int c = 32; c < 64; ++c) pk[c] = f16x2_to_bf16x2(pk[c]);
       }
       tmem_store_32cols(tY + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
       tmem_store_32cols(tY + 64, *reinterpret_cast<const uint32_t(*)[32]>(&dk[0]));
@@ -1141,8 +1242,14 @@ __device__ __forceinline__ void dkvf_elem(const BwdParams& p, uint32_t sbase, ui
     tc_fence_after_sync();
     const bool key_ok = key < p.N;
     const size_t krow = (static_cast<size_t>(it.b) * p.Hkv + it.hkv) * p.N + (key_ok ? key : 0);
-    store_acc_row<D>(t_dv, 1.f, p.dv + krow * D, key_ok);
-    store_acc_row<D>(t_dk, p.scale, p.dk + krow * D, key_ok);
+    if (SINK && it.part >= 0) {
+      float* dst = p.part + (static_cast<size_t>(it.part) * 2 * kTile + r) * D;
+      store_acc_row_f32<D>(t_dv, dst);
+      store_acc_row_f32<D>(t_dk, dst + kTile * D);
+    } else {
+      store_acc_row<D>(t_dv, 1.f, p.dv + krow * D, key_ok);
+      store_acc_row<D>(t_dk, p.scale, p.dk + krow * D, key_ok);
+    }
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(L::kAccFree));
@@ -1155,7 +1262,7 @@ __device__ __forceinline__ void dkvf_elem(const BwdParams& p, uint32_t sbase, ui
 // (thread = TMEM lane = column c of dQ, 64 query values) and add it into the
 // fp32 accumulator: for each query, the warp's 32 lanes add 32 consecutive
 // floats (one 128-byte reduction).
-template <int D>
+template <int D, bool SINK>
 __device__ __forceinline__ void dkv_dq(const BwdParams& p, uint32_t sbase, uint32_t tmem, const BwdWaiter& w,
                                        int warp, int lane) {
   using L = BwdSmem<D>;
@@ -1167,7 +1274,7 @@ __device__ __forceinline__ void dkv_dq(const BwdParams& p, uint32_t sbase, uint3
   uint32_t cnt[2] = {0, 0};
   bool ok = true;
   for (int i = blockIdx.x; ok && i < p.num_items; i += gridDim.x) {
-    const DkvItem it = dkv_item(p, i);
+    const DkvItem it = dkv_item<SINK>(p, i);
     for (int s = 0; s < it.steps && ok; ++s) {
       int hq, m;
       dkv_step(p, it, s, hq, m);
@@ -1213,13 +1320,37 @@ __global__ void __launch_bounds__(256) attn_bwd_dq_convert_kernel(const float* _
   }
 }
 
+// Sink tiles of the SINK key-tile kernels: dV and dK of each row are the sums of its
+// sink_parts partial rows, added in their order.  One thread per four columns; blockIdx.x =
+// (b, KV head, sink tile) and dV or dK.
+template <int D>
+__global__ void __launch_bounds__(256) attn_bwd_sink_reduce_kernel(const __grid_constant__ BwdParams p) {
+  const int t = blockIdx.y * 256 + threadIdx.x, r = t / (D / 4), c = t % (D / 4) * 4;
+  const int which = blockIdx.x & 1, tile = blockIdx.x >> 1;  // tile = bk * sink_tiles + n
+  const int bk = tile / p.sink_tiles, key = (tile - bk * p.sink_tiles) * kTile + r;
+  if (r >= kTile || key >= p.N) return;
+  const float* src = p.part + ((static_cast<size_t>(tile) * p.sink_parts * 2 + which) * kTile + r) * D + c;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < p.sink_parts; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(src + static_cast<size_t>(k) * 2 * kTile * D);
+    sum.x += x.x;
+    sum.y += x.y;
+    sum.z += x.z;
+    sum.w += x.w;
+  }
+  const float mul = which ? p.scale : 1.f;
+  __nv_bfloat16* dst = (which ? p.dk : p.dv) + (static_cast<size_t>(bk) * p.N + key) * D + c;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_rn(sum.x * mul, sum.y * mul), bf16x2_rn(sum.z * mul, sum.w * mul));
+}
+
 // ------------------------------------------------------------------ entry
 template <int KIND>
 constexpr int bwd_threads() {
   return KIND == kBKernelFused ? kBwdThreadsFused : kBwdThreads;
 }
 
-template <int D, int KIND>
+// SINK: the sliding window with sinks, as instances of their own.
+template <int D, int KIND, bool SINK = false>
 __global__ void __launch_bounds__(bwd_threads<KIND>(), 1) __maxnreg__(KIND == kBKernelFused ? 200 : 255) attn_bwd_kernel(const __grid_constant__ BwdParams p) {
   using L = BwdSmem<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -1267,21 +1398,21 @@ __global__ void __launch_bounds__(bwd_threads<KIND>(), 1) __maxnreg__(KIND == kB
   const uint32_t tmem = *tmem_slot;
   const BwdWaiter w{p.timeout_ns, abort_flag, p.err};
   if (warp < 4) {
-    if constexpr (KIND == kBKernelDqFull) dqf_elem<D>(p, sbase, tmem, w, warp, lane);
-    else if constexpr (KIND == kBKernelDkdvFull) dkvf_elem<D>(p, sbase, tmem, w, warp, lane);
-    else dkv_elem<D>(p, sbase, tmem, w, warp, lane);
+    if constexpr (KIND == kBKernelDqFull) dqf_elem<D, SINK>(p, sbase, tmem, w, warp, lane);
+    else if constexpr (KIND == kBKernelDkdvFull) dkvf_elem<D, SINK>(p, sbase, tmem, w, warp, lane);
+    else dkv_elem<D, SINK>(p, sbase, tmem, w, warp, lane);
   } else if (warp >= kBwdDqWarp0) {
-    if constexpr (KIND == kBKernelFused) dkv_dq<D>(p, sbase, tmem, w, warp, lane);
+    if constexpr (KIND == kBKernelFused) dkv_dq<D, SINK>(p, sbase, tmem, w, warp, lane);
   } else if (warp == kBwdLoaderWarp) {
     if (lane == 0) {
-      if (KIND == kBKernelDqFull) dq_loader<D>(p, sbase, w);
-      else dkv_loader<D, KIND == kBKernelDkdvFull>(p, sbase, w);
+      if (KIND == kBKernelDqFull) dq_loader<D, SINK>(p, sbase, w);
+      else dkv_loader<D, KIND == kBKernelDkdvFull, SINK>(p, sbase, w);
     }
     __syncwarp();
   } else if (warp == kBwdMmaWarp) {
-    if constexpr (KIND == kBKernelDqFull) dqf_mma<D>(p, sbase, tmem, w);
-    else if constexpr (KIND == kBKernelDkdvFull) dkvf_mma<D>(p, sbase, tmem, w);
-    else dkv_mma<D>(p, sbase, tmem, w);
+    if constexpr (KIND == kBKernelDqFull) dqf_mma<D, SINK>(p, sbase, tmem, w);
+    else if constexpr (KIND == kBKernelDkdvFull) dkvf_mma<D, SINK>(p, sbase, tmem, w);
+    else dkv_mma<D, SINK>(p, sbase, tmem, w);
     // Every MMA this warp issued must complete before TMEM is freed.
     tc_commit_elect(sbase + L::kBarOff + 8u * L::kFin);
     w.drain(sbase + L::kBarOff + 8u * L::kFin, 0, (KIND << 12) | (kBRoleMma << 8) | L::kFin);

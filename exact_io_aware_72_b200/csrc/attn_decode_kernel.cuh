@@ -612,8 +612,11 @@ __device__ __forceinline__ void dec_softmax(const DecParams& p, uint32_t sbase, 
           // Masked scores are replaced (not offset), so whatever an unloaded
           // or stale slot produced never reaches P.
 #pragma unroll
-          for (int c = 0; c < C; ++c)
-            x[c] = ((key0 + c >= lo_vis || key0 + c < it.sinks) && key0 + c <= hi_vis) ? x[c] : -INFINITY;
+          for (int c0 = 0; c0 < C; c0 += 32) {
+            const uint32_t seen = seen_bits(key0 + c0, lo_vis, hi_vis + 1, it.sinks);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c0 + c] = (seen & (1u << c)) ? x[c0 + c] : -INFINITY;
+          }
         }
       }
       float mx = x[0];

@@ -742,10 +742,19 @@ __device__ __forceinline__ void softmax_role(const FwdParams& p, uint32_t sbase,
           const int c0 = j * kBlockN;
           const int hi_i = ((p.mask_kind == kMaskFull) ? p.N - 1 : min(row + p.key_offset, p.N - 1)) - c0;
           const int lo_i = (p.mask_kind == kMaskWindow) ? row + p.key_offset - p.window + 1 - c0 : -1;
-          const int sink_i = SINK ? p.sinks - c0 : 0;  // keys of the tile below it are sinks
+          if constexpr (SINK) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i > hi_i || (i < lo_i && !(SINK && i < sink_i))) s[i] = -INFINITY;
+            for (int w32 = 0; w32 < 4; ++w32) {
+              const uint32_t seen = seen_bits(32 * w32, lo_i, hi_i + 1, p.sinks - c0);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(seen & (1u << i))) s[32 * w32 + i] = -INFINITY;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i > hi_i || i < lo_i) s[i] = -INFINITY;
+          }
         }
       }
       bool need = false;

@@ -354,6 +354,17 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// The low n bits (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+// Bits 0 .. 31 of the columns base .. base + 31 that a row sees: those below `end` that lie from
+// `lo` on or below `sink`.  (Masks with sinks are two ranges; testing a bit takes one
+// instruction per column, where the comparisons became branches: 40 % of a forward.)
+__device__ __forceinline__ uint32_t seen_bits(int base, int lo, int end, int sink) {
+  return low_bits(end - base) & (~low_bits(lo - base) | low_bits(sink - base));
+}
+
 // Packed fp32 pairs (sm_100): one instruction operates on two floats.
 __device__ __forceinline__ uint64_t f32x2_pack(float lo, float hi) {
   uint64_t r;

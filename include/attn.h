@@ -296,6 +296,13 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
    4 B Hq N 128 (the d = 128 dQ accumulator); 0 for invalid sizes or a total beyond 2^61. */
 size_t attn_bwd_workspace_bytes(int64_t B, int64_t Hq, int64_t N);
 
+/* Workspace bytes attn_bwd_ex needs with the sliding window and sinks > 0, 16-byte aligned (0 for
+   invalid sizes): attn_bwd_workspace_bytes and room for the fp32 partial sums of the key tiles
+   that hold sinks, whose queries are cut into parts (a smaller workspace is refused). dk and dv
+   stay bitwise reproducible: the parts are added in a fixed order. */
+size_t attn_bwd_sink_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t d, int64_t window,
+                                     int64_t sinks);
+
 /* attn_debug_error for the backward kernels' error word (same contract). */
 int attn_bwd_debug_error(cudaStream_t stream, int* device_code);
 /*
