@@ -24,19 +24,25 @@
 //   the softmax threads, 16 rows (16 bytes) per key.  E4M3 V needs an 8-bit P: the weight is
 //   held as a sum of three E5M2 numbers (3 significant bits each, 9 together: off by at most
 //   2^-9, half of a bf16 weight's rounding), three products into one accumulator.  Weights are
-//   scaled so that m sits at 2^11: they reach 2^15 before m must move (E5M2 ends at 57344),
-//   and a weight is lost only below 2^-28 of the largest.
+//   scaled so that m sits at 2^9: they reach 2^15 before m must move (E5M2 ends at 57344),
+//   and a weight is lost only below 2^-26 of the largest.
 // * Sums l and all statistics are fp32; out is rounded once to bf16.
 //
 // Work items, splits and the item counter are the bf16 decoding kernel's.  Two softmax
 // warpgroups take the tiles of an item in turn, each with its own m, l and O, merged at the
 // item's end.  m is per row and warpgroup: a vote over the warpgroup (one hardware barrier
-// with a reduction) finds the rare tiles where some row's maximum grew by more than 2^4.
+// with a reduction) finds the rare tiles where some row's maximum grew by more than 2^6.
 //
-// Warps: 0-3 and 4-7 softmax, 8 loads K (and fetches items), 9 loads V, 10 issues the
-// products, 11 prepares Q.  TMEM: four S buffers, then the two O.  All mbarrier waits are
-// bounded; the warpgroup barriers are reached by every warp whether or not a wait gave up,
-// and carry that news, so the roles leave together.
+// The splits of one (sequence, KV head, row chunk) count themselves in the workspace as they
+// finish, and the CTA that finishes the last one merges their partial results, in the order
+// of the splits (a merge launch of its own took 9 us behind a 70 us step).
+//
+// Warps: 0-3 and 4-7 softmax, 8 loads K (and fetches items), 9 loads V, 10 issues the P V
+// products, 11 prepares Q and issues the S products up to four tiles ahead.  (One issuing
+// warp spent 1500 cycles per tile on waits and issue latencies of both products, whose
+// execution takes 340; HBM delivers a tile per 1400.)  TMEM: four S buffers, then the two
+// O.  All mbarrier waits are bounded; the warpgroup barriers are reached by every warp
+// whether or not a wait gave up, and carry that news, so the roles leave together.
 #pragma once
 
 #include <cuda.h>
@@ -59,16 +65,16 @@ using attn_sm100_dec::kDMaskWindow;
 using attn_sm100_dec::kDRoleLoader;
 using attn_sm100_dec::kDRoleMma;
 using attn_sm100_dec::kDRoleSoftmax;
-constexpr int kDRoleQ = 4;
+constexpr int kDRoleS = 4;
 
 constexpr int kKeys = 128;  // keys per tile
 constexpr int kThreads = 384;
 constexpr int kWg = 128;    // threads of a softmax warpgroup
-constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kQWarp = 11;
+constexpr int kKWarp = 8, kVWarp = 9, kPvWarp = 10, kSWarp = 11;
 constexpr int kItemSlots = 4;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kTop = 11.f;     // weights at the running maximum are 2^kTop
-constexpr float kGrow = 4.f;     // the running maximum moves when a row's grows by more
+constexpr float kTop = 9.f;      // weights at the running maximum are 2^kTop
+constexpr float kGrow = 6.f;     // the running maximum moves when a row's grows by more
 constexpr float kNoMax = -1e30f; // running maximum of a row that has seen no key
 constexpr float kScaleMin = 9.094947017729282e-13f, kScaleMax = 1099511627776.f;  // 2^-40, 2^40
 
@@ -94,6 +100,7 @@ struct Dec8Params {
   float scale_log2;
   unsigned long long timeout_ns;
   unsigned int* sched;     // [0] next work item, [1] CTAs finished; zero between launches
+  unsigned int* done;      // splits finished, per (b, KV head, row chunk); zero between launches (null: no merge here)
 };
 
 template <int D, int NR>
@@ -124,11 +131,12 @@ struct Smem8 {
   static constexpr int kKVFull = 4;
   static constexpr int kKVEmpty = kKVFull + kStages;
   static constexpr int kSFull = kKVEmpty + kStages;    // x4
-  static constexpr int kPFull = kSFull + 4;            // x2, one per warpgroup
+  static constexpr int kSFree = kSFull + 4;            // x4
+  static constexpr int kPFull = kSFree + 4;            // x2, one per warpgroup
   static constexpr int kPVDone = kPFull + 2;           // x2
   static constexpr int kOFree = kPVDone + 2;
-  static constexpr int kFin = kOFree + 1;
-  static constexpr int kItemFull = kFin + 1;
+  static constexpr int kFin = kOFree + 1;              // x2, one per issuing warp
+  static constexpr int kItemFull = kFin + 2;
   static constexpr int kItemEmpty = kItemFull + kItemSlots;
   static constexpr int kNumBars = kItemEmpty + kItemSlots;
   static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
@@ -136,8 +144,14 @@ struct Smem8 {
   static constexpr uint32_t kBytes = kItemOff + 4 * kItemSlots;
   static constexpr uint32_t kAlloc = 232448;
   static_assert(kBytes - kFrOff <= kSmall && kBytes + 1024 <= kAlloc, "shared memory per CTA");
-  static constexpr uint32_t kSCol = 0, kOCol = 4 * NR;          // + NR per buffer / warpgroup
-  static constexpr uint32_t kTmemCols = NR == 16 ? 128 : (NR == 32 ? 256 : 512);
+  // The terms of Q and of P are side by side in one product's N where TMEM has room for
+  // their separate sums (a product of few rows takes the time of reading its A operand, 128
+  // rows, whatever N is), and further products into the same sums otherwise.
+  static constexpr bool kWide = NR <= 32;
+  static constexpr uint32_t kSCols = kWide ? 2 * NR : NR, kOCols = kWide ? 3 * NR : NR;
+  static constexpr uint32_t kSCol = 0, kOCol = 4 * kSCols;      // + kSCols per buffer, kOCols per warpgroup
+  static constexpr uint32_t kTmemCols = NR == 16 ? 256 : 512;
+  static_assert(4 * kSCols + 2 * kOCols <= kTmemCols, "TMEM columns");
 };
 
 // ------------------------------------------------------------ work items
@@ -219,6 +233,18 @@ __device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[1
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load_2x16cols(uint32_t ta, uint32_t tb, uint32_t (&a)[16], uint32_t (&b)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
+        "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(b[0]),
+        "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]),
+        "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
+      : "r"(ta), "r"(tb)
       : "memory");
 }
 __device__ __forceinline__ void tma_load_3d_first(uint32_t dst, const CUtensorMap* map, uint32_t bar, int y, int z,
@@ -337,103 +363,86 @@ __device__ __forceinline__ void drain_ring8(uint32_t sbase, const DecWaiter& w, 
 }
 
 // ------------------------------------------------------------ Q
-// One warp: each row of the next item becomes two E4M3 terms in shared memory (K-major, in
-// the swizzle of a D-byte row), with its factor scale log2(e) / (the row's power of two).
+// One warp: each row of an item becomes two E4M3 terms in shared memory (K-major, in the
+// swizzle of a D-byte row), with its factor scale log2(e) / (the row's power of two).
 template <int D, int NR>
-__device__ __forceinline__ void q_role8(const Dec8Params& p, uint32_t sbase, uint8_t* smem, const DecWaiter& w) {
+__device__ __forceinline__ void prepare_q8(const Dec8Params& p, const Item8& it, uint8_t* smem, uint32_t buf) {
   using L = Smem8<D, NR>;
-  auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
   const int lane = threadIdx.x & 31;
-  const int code = kDRoleQ << 8;
-  uint32_t k_item = 0, n = 0;
-  while (true) {
-    const int idx = take_item8<L>(sbase, smem, w, k_item, code);
-    if (idx < 0) break;
-    const Item8 it = item8(p, idx);
-    if (it.t1 < it.t0) continue;
-    const uint32_t buf = n & 1;
-    if (n >= 2 && !w.wait_warp(bar(L::kQEmpty + buf), ((n >> 1) - 1) & 1, code | (L::kQEmpty + buf))) break;
-    const size_t row = (static_cast<size_t>(it.b) * p.Hq + static_cast<size_t>(it.hkv) * p.group) * p.Nq + it.row0;
-    const __nv_bfloat16* src = p.q + row * D;
-    float* fr = reinterpret_cast<float*>(smem + L::kFrOff) + buf * NR;
-    uint8_t* q1 = smem + L::kQOff + buf * L::kQBuf;
-    constexpr int E = D / 32;  // elements of a lane
+  const size_t row = (static_cast<size_t>(it.b) * p.Hq + static_cast<size_t>(it.hkv) * p.group) * p.Nq + it.row0;
+  const __nv_bfloat16* src = p.q + row * D;
+  float* fr = reinterpret_cast<float*>(smem + L::kFrOff) + buf * NR;
+  uint8_t* q1 = smem + L::kQOff + buf * L::kQBuf;
+  constexpr int E = D / 32;  // elements of a lane
 #pragma unroll 8
-    for (int r = 0; r < NR; ++r) {
-      float x[E];
+  for (int r = 0; r < NR; ++r) {
+    float x[E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = 0.f;
-      if (r < it.rows) {
-        const uint32_t* s32 = reinterpret_cast<const uint32_t*>(src + static_cast<size_t>(r) * D) + lane * (E / 2);
+    for (int i = 0; i < E; ++i) x[i] = 0.f;
+    if (r < it.rows) {
+      const uint32_t* s32 = reinterpret_cast<const uint32_t*>(src + static_cast<size_t>(r) * D) + lane * (E / 2);
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          const uint32_t v = __ldg(s32 + i);
-          x[2 * i] = __uint_as_float(v << 16);
-          x[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
-        }
+      for (int i = 0; i < E / 2; ++i) {
+        const uint32_t v = __ldg(s32 + i);
+        x[2 * i] = __uint_as_float(v << 16);
+        x[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
       }
-      uint32_t big = 0;
-#pragma unroll
-      for (int i = 0; i < E; ++i) big = max(big, __float_as_uint(x[i]) & 0x7fffffffu);
-      big = __reduce_max_sync(0xffffffffu, big);
-      // Multiplier 2^(7 - exponent): the row's largest lands in [128, 256).
-      const int e = static_cast<int>(big >> 23) - 127;
-      const int mul_e = min(max(7 - e, -126), 126);
-      float mul = big ? __uint_as_float(static_cast<uint32_t>(mul_e + 127) << 23) : 1.f;
-      if (big >= 0x7f800000u) mul = __int_as_float(0x7fffffff);  // E4M3 has no infinities: the row becomes NaN
-      float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < E; ++i) hi[i] = x[i] * mul;
-      const uint32_t c1 = pack_e4m3x4(hi[0], hi[1], hi[2], hi[3]);
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        uint32_t h2;
-        float f;
-        asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}"
-            : "=r"(h2)
-            : "r"((c1 >> (8 * i)) & 0xffu));
-        asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h2));
-        lo[i] = hi[i] - f;
-      }
-      const uint32_t c2 = pack_e4m3x4(lo[0], lo[1], lo[2], lo[3]);
-      if constexpr (D == 128) {
-        const uint32_t at = r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-        *reinterpret_cast<uint32_t*>(q1 + at) = c1;
-        *reinterpret_cast<uint32_t*>(q1 + L::kQTerm + at) = c2;
-      } else {
-        const uint32_t at = r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2;
-        *reinterpret_cast<uint16_t*>(q1 + at) = static_cast<uint16_t>(c1);
-        *reinterpret_cast<uint16_t*>(q1 + L::kQTerm + at) = static_cast<uint16_t>(c2);
-      }
-      if (lane == 0) fr[r] = p.scale_log2 / mul;
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(L::kQFull + buf));
-    ++n;
+    uint32_t big = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) big = max(big, __float_as_uint(x[i]) & 0x7fffffffu);
+    big = __reduce_max_sync(0xffffffffu, big);
+    // Multiplier 2^(7 - exponent): the row's largest lands in [128, 256).
+    const int e = static_cast<int>(big >> 23) - 127;
+    const int mul_e = min(max(7 - e, -126), 126);
+    float mul = big ? __uint_as_float(static_cast<uint32_t>(mul_e + 127) << 23) : 1.f;
+    if (big >= 0x7f800000u) mul = __int_as_float(0x7fffffff);  // E4M3 has no infinities: the row becomes NaN
+    float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < E; ++i) hi[i] = x[i] * mul;
+    const uint32_t c1 = pack_e4m3x4(hi[0], hi[1], hi[2], hi[3]);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      uint32_t h2;
+      float f;
+      asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}"
+          : "=r"(h2)
+          : "r"((c1 >> (8 * i)) & 0xffu));
+      asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h2));
+      lo[i] = hi[i] - f;
+    }
+    const uint32_t c2 = pack_e4m3x4(lo[0], lo[1], lo[2], lo[3]);
+    if constexpr (D == 128) {
+      const uint32_t at = r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+      *reinterpret_cast<uint32_t*>(q1 + at) = c1;
+      *reinterpret_cast<uint32_t*>(q1 + L::kQTerm + at) = c2;
+    } else {
+      const uint32_t at = r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2;
+      *reinterpret_cast<uint16_t*>(q1 + at) = static_cast<uint16_t>(c1);
+      *reinterpret_cast<uint16_t*>(q1 + L::kQTerm + at) = static_cast<uint16_t>(c2);
+    }
+    if (lane == 0) fr[r] = p.scale_log2 / mul;
   }
+  fence_proxy_async_smem();
+  __syncwarp();
 }
 
 // ------------------------------------------------------------ products
-// Per tile j: S^T_j = K_j (Q1 + Q2)^T two tiles ahead of O_w += V_j^T (P1 + P2 + P3), w the
-// tile's warpgroup.
+// S^T_j = K_j (Q1 + Q2)^T for every tile of every item, as far ahead as K, the four S buffers
+// and the two Q buffers allow.
 template <int D, int NR>
-__device__ __forceinline__ void mma_role8(const Dec8Params& p, uint32_t sbase, const uint8_t* smem, uint32_t tmem,
-                                          const DecWaiter& w) {
+__device__ __forceinline__ void s_role8(const Dec8Params& p, uint32_t sbase, uint8_t* smem, uint32_t tmem,
+                                        const DecWaiter& w) {
   using L = Smem8<D, NR>;
   auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
   constexpr uint32_t kLayout = D == 128 ? 2 : 4;   // 128- or 64-byte swizzle: one row per line
   constexpr uint32_t kAtom = 8 * D;                // eight rows
-  constexpr uint32_t idesc_s = idesc8(NR, 0, 0, false, false);
-  constexpr uint32_t idesc_o = idesc8(NR, 0, 1, true, true);
+  constexpr uint32_t idesc_s = idesc8(L::kSCols, 0, 0, false, false);
+  constexpr int kProducts = L::kWide ? 1 : 2;
   const uint64_t k_desc0 = desc8(sbase + L::kRingOff, 16, kAtom, kLayout);
-  // V^T: M runs along a row.  With d = 64 the rows end after 64, and a stride of 0 to the
-  // next 64 lets lanes 64 .. 127 repeat lanes 0 .. 63.
-  const uint64_t v_desc0 = desc8(sbase + L::kRingOff, 0, kAtom, kLayout);
   const uint64_t q_desc0 = desc8(sbase + L::kQOff, 16, kAtom, kLayout);
-  // P: units of 16 rows, 16 bytes per key; eight keys are a core matrix.
-  const uint64_t p_desc0 = desc8(sbase + L::kPOff, 128, kKeys * 16, 0);
-  const int code = kDRoleMma << 8;
+  const bool leader = elect_one();  // issues the products, so that the commits track them
+  const int code = kDRoleS << 8;
   uint32_t g = 0, items = 0, k_item = 0;
   bool ok = true;
   while (ok) {
@@ -443,41 +452,67 @@ __device__ __forceinline__ void mma_role8(const Dec8Params& p, uint32_t sbase, c
     if (it.t1 < it.t0) continue;
     const int n = it.t1 - it.t0 + 1;
     const uint32_t qbuf = items & 1;
-    if (!w.wait_warp(bar(L::kQFull + qbuf), (items >> 1) & 1, code | (L::kQFull + qbuf))) break;
-    tc_fence_after_sync();
+    if (items >= 2 && !w.wait_warp(bar(L::kQEmpty + qbuf), ((items >> 1) - 1) & 1, code | (L::kQEmpty + qbuf))) break;
+    prepare_q8<D, NR>(p, it, smem, qbuf);
+    if (leader) mbar_arrive(bar(L::kQFull + qbuf));
     const uint64_t qd = q_desc0 + ((qbuf * L::kQBuf) >> 4);
-    int s_next = 0;  // next tile whose S is to be issued
-    auto k_landed = [&](int j) -> bool {
-      const uint32_t ki = 2 * (g + j), slot = ki % L::kStages;
-      return __all_sync(0xffffffffu, mbar_try_wait(bar(L::kKVFull + slot), (ki / L::kStages) & 1));
-    };
-    auto issue_s = [&]() -> bool {
-      const uint32_t gi = g + s_next, ki = 2 * gi, slot = ki % L::kStages;
-      if (!w.wait_warp(bar(L::kKVFull + slot), (ki / L::kStages) & 1, code | (L::kKVFull + slot))) return false;
-      tc_fence_after_sync();
-      const uint32_t s_tmem = tmem + L::kSCol + (gi & 3) * NR;
-      const uint64_t kd = k_desc0 + ((slot * L::kTileBytes) >> 4);
-#pragma unroll
-      for (int term = 0; term < 2; ++term)
-#pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk)
-          mma_e4m3_ss_elect(s_tmem, kd + ((kk * 32) >> 4), qd + ((term * L::kQTerm + kk * 32) >> 4), idesc_s,
-                            (term | kk) ? 1u : 0u);
-      tc_commit_elect(bar(L::kSFull + (gi & 3)));
-      tc_commit_elect(bar(L::kKVEmpty + slot));
-      ++s_next;
-      if (s_next == n) tc_commit_elect(bar(L::kQEmpty + qbuf));
-      return true;
-    };
-    if (!issue_s()) break;
-    if (n > 1 && k_landed(1) && !issue_s()) break;
-    uint32_t started = 0;  // warpgroups whose O holds tiles of this item
     for (int j = 0; j < n; ++j) {
-      // S may run up to two tiles ahead where K has landed (S buffer gi & 3 was last read
-      // before P of tile gi - 4 was published); the tile after this one must be issued
-      // before P of it can be waited for.
-      while (ok && s_next < n && s_next <= j + 2 && k_landed(s_next)) ok = issue_s();
-      if (!ok) break;
+      const uint32_t gi = g + j, ki = 2 * gi, slot = ki % L::kStages;
+      if ((gi >= 4 && !w.wait_warp(bar(L::kSFree + (gi & 3)), ((gi >> 2) - 1) & 1, code | (L::kSFree + (gi & 3)))) ||
+          !w.wait_warp(bar(L::kKVFull + slot), (ki / L::kStages) & 1, code | (L::kKVFull + slot))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t s_tmem = tmem + L::kSCol + (gi & 3) * L::kSCols;
+      const uint64_t kd = k_desc0 + ((slot * L::kTileBytes) >> 4);
+      if (leader) {
+#pragma unroll
+        for (int term = 0; term < kProducts; ++term)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_f8f6f4_ss(s_tmem, kd + ((kk * 32) >> 4), qd + ((term * L::kQTerm + kk * 32) >> 4), idesc_s,
+                          (term | kk) ? 1u : 0u);
+        tc_commit(bar(L::kSFull + (gi & 3)));
+        tc_commit(bar(L::kKVEmpty + slot));
+        if (j == n - 1) tc_commit(bar(L::kQEmpty + qbuf));
+      }
+      __syncwarp();
+    }
+    g += n;
+    ++items;
+  }
+  // Every product this warp issued must complete before TMEM is freed.
+  if (leader) tc_commit(bar(L::kFin));
+  __syncwarp();
+  w.drain(bar(L::kFin), 0, code | L::kFin);
+}
+
+// O_w += V_j^T (P1 + P2 + P3), w the tile's warpgroup.
+template <int D, int NR>
+__device__ __forceinline__ void pv_role8(const Dec8Params& p, uint32_t sbase, const uint8_t* smem, uint32_t tmem,
+                                         const DecWaiter& w) {
+  using L = Smem8<D, NR>;
+  auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
+  constexpr uint32_t kLayout = D == 128 ? 2 : 4;
+  constexpr uint32_t idesc_o = idesc8(L::kOCols, 0, 1, true, true);
+  constexpr int kProducts = L::kWide ? 1 : 3;
+  // V^T: M runs along a row.  With d = 64 the rows end after 64, and a stride of 0 to the
+  // next 64 lets lanes 64 .. 127 repeat lanes 0 .. 63.
+  const uint64_t v_desc0 = desc8(sbase + L::kRingOff, 0, 8 * D, kLayout);
+  // P: units of 16 rows, 16 bytes per key; eight keys are a core matrix.
+  const uint64_t p_desc0 = desc8(sbase + L::kPOff, 128, kKeys * 16, 0);
+  const bool leader = elect_one();
+  const int code = kDRoleMma << 8;
+  uint32_t g = 0, items = 0, k_item = 0;
+  bool ok = true;
+  while (ok) {
+    const int idx = take_item8<L>(sbase, smem, w, k_item, code);
+    if (idx < 0) break;
+    const Item8 it = item8(p, idx);
+    if (it.t1 < it.t0) continue;
+    const int n = it.t1 - it.t0 + 1;
+    for (int j = 0; j < n; ++j) {
       const uint32_t gi = g + j, wg = gi & 1, vi = 2 * gi + 1, slot = vi % L::kStages;
       if (!w.wait_warp(bar(L::kPFull + wg), (gi >> 1) & 1, code | (L::kPFull + wg)) ||
           !w.wait_warp(bar(L::kKVFull + slot), (vi / L::kStages) & 1, code | (L::kKVFull + slot)) ||
@@ -486,27 +521,28 @@ __device__ __forceinline__ void mma_role8(const Dec8Params& p, uint32_t sbase, c
         break;
       }
       tc_fence_after_sync();
-      const uint32_t o_tmem = tmem + L::kOCol + wg * NR;
+      const uint32_t o_tmem = tmem + L::kOCol + wg * L::kOCols;
       const uint64_t vd = v_desc0 + ((slot * L::kTileBytes) >> 4);
       const uint64_t pd = p_desc0 + ((wg * L::kPBuf) >> 4);
-      const uint32_t fresh = (started >> wg & 1) ? 1u : 0u;
+      const uint32_t more = j >= 2 ? 1u : 0u;  // each warpgroup's first tile of the item starts its O
+      if (leader) {
 #pragma unroll
-      for (int term = 0; term < 3; ++term)
+        for (int term = 0; term < kProducts; ++term)
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 32; ++kk)
-          mma_e4m3_ss_elect(o_tmem, vd + ((kk * 32 * D) >> 4), pd + ((term * L::kPTerm + kk * 32 * 16) >> 4), idesc_o,
-                            (term | kk) ? 1u : fresh);
-      started |= 1u << wg;
-      tc_commit_elect(bar(L::kPVDone + wg));
-      tc_commit_elect(bar(L::kKVEmpty + slot));
-      if (j + 1 < n && s_next == j + 1) ok = issue_s();
-      if (!ok) break;
+          for (int kk = 0; kk < kKeys / 32; ++kk)
+            mma_f8f6f4_ss(o_tmem, vd + ((kk * 32 * D) >> 4), pd + ((term * L::kPTerm + kk * 32 * 16) >> 4), idesc_o,
+                          (term | kk) ? 1u : more);
+        tc_commit(bar(L::kPVDone + wg));
+        tc_commit(bar(L::kKVEmpty + slot));
+      }
+      __syncwarp();
     }
     g += n;
     ++items;
   }
-  tc_commit_elect(bar(L::kFin));
-  w.drain(bar(L::kFin), 0, code | L::kFin);
+  if (leader) tc_commit(bar(L::kFin + 1));
+  __syncwarp();
+  w.drain(bar(L::kFin + 1), 0, code | (L::kFin + 1));
 }
 
 // ------------------------------------------------------------ softmax
@@ -542,6 +578,52 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
     if (idx < 0) break;
     const Item8 it = item8(p, idx);
     const size_t grow0 = (static_cast<size_t>(it.b) * p.Hq + static_cast<size_t>(it.hkv) * p.group) * p.Nq + it.row0;
+    // This item's partial result is written: the CTA whose item is the last of its rows to get
+    // here merges all S of them (out = sum_s w_s O_s / sum_s w_s, w_s = 2^(lse2_s - max)), four
+    // columns of a row per thread.
+    auto merge_if_last = [&]() {
+      if (!p.done) return;
+      __threadfence();
+      bool last = false;
+      bar_or(3, 2 * kWg, false);
+      if (tid == 0) {
+        unsigned int* count = p.done + idx / S;
+        last = atomicAdd(count, 1u) == static_cast<unsigned>(S - 1);
+        if (last) atomicExch(count, 0u);
+        __threadfence();
+      }
+      if (!bar_or(3, 2 * kWg, last)) return;
+      constexpr int Q = D / 4;
+      for (int t = tid; t < it.rows * Q; t += 2 * kWg) {
+        const size_t row = grow0 + t / Q;
+        const int c = t % Q * 4;
+        const float* pl = p.part_lse + row * S;
+        const float* po = p.part_o + row * S * D + c;
+        float top = -INFINITY;
+        for (int k = 0; k < S; ++k) top = fmaxf(top, __ldcg(pl + k));
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float wsum = 0.f;
+        const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+        for (int k = 0; k < S; ++k) {
+          const float l2 = __ldcg(pl + k), wgt = dec_exp2(l2 - base);
+          if (l2 != -INFINITY) {   // a split that saw nothing wrote no O
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(po + static_cast<size_t>(k) * D));
+            wsum += wgt;
+            sum.x = fmaf(wgt, o.x, sum.x);
+            sum.y = fmaf(wgt, o.y, sum.y);
+            sum.z = fmaf(wgt, o.z, sum.z);
+            sum.w = fmaf(wgt, o.w, sum.w);
+          }
+        }
+        const float inv = wsum != 0.f ? 1.f / wsum : 0.f;
+        uint2 h;
+        h.x = attn_sm100_dec::dec_pack_bf16x2(sum.x * inv, sum.y * inv);
+        h.y = attn_sm100_dec::dec_pack_bf16x2(sum.z * inv, sum.w * inv);
+        *reinterpret_cast<uint2*>(p.out + row * D + c) = h;
+        if (c == 0) p.lse[row] = wsum != 0.f ? (top + __log2f(wsum)) * kLn2 : -INFINITY;
+      }
+    };
     if (it.t1 < it.t0) {
       if (it.bad && tid == 0) atomicCAS(p.err, 0, kDErrSeqLen | (it.b & 0xFFFFF));
       for (int e = tid; e < it.rows; e += 2 * kWg) {
@@ -552,6 +634,7 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
           for (int c = 0; c < D; ++c) p.out[(grow0 + e) * D + c] = __float2bfloat16_rn(0.f);
         }
       }
+      if (S > 1) merge_if_last();
       continue;
     }
     const int n = it.t1 - it.t0 + 1;
@@ -607,17 +690,24 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       const int base = it.tile(it.t0 + j) * kKeys, pos = base + key;
       const bool whole = base + kKeys - 1 <= all_hi && (base >= all_lo || base + kKeys <= it.sinks);
       const float vsc = fminf(fmaxf(vs, kScaleMin), kScaleMax);
-      const float lv = __log2f(vsc), ivs = 1.f / vsc;
+      const float lv = __log2f(vsc), ivs = __frcp_rn(vsc);
       if (!failed) failed = !w.wait_warp(bar(L::kSFull + (gi & 3)), (gi >> 2) & 1, code | (L::kSFull + (gi & 3)));
       // The previous P V of this warpgroup is done: its P may be overwritten and O rescaled.
       if (!failed && (gi >> 1) > 0)
         failed = !w.wait_warp(bar(L::kPVDone + wg), ((gi >> 1) - 1) & 1, code | (L::kPVDone + wg));
       tc_fence_after_sync();
-      const uint32_t s_addr = lane_addr + L::kSCol + (gi & 3) * NR;
+      const uint32_t s_addr = lane_addr + L::kSCol + (gi & 3) * L::kSCols;
       // e[i] = y - m + kTop of rows 16 ch + i (the exponent of the weight), -inf where masked.
       auto exponents = [&](int ch, float add, bool with_m, float (&e)[16]) {
         uint32_t sr[16];
-        tmem_load_16cols(s_addr + ch * 16, sr);
+        if constexpr (L::kWide) {
+          uint32_t s2[16];
+          tmem_load_2x16cols(s_addr + ch * 16, s_addr + NR + ch * 16, sr, s2);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sr[i] = __float_as_uint(__uint_as_float(sr[i]) + __uint_as_float(s2[i]));
+        } else {
+          tmem_load_16cols(s_addr + ch * 16, sr);
+        }
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 f4 = *reinterpret_cast<const float4*>(fr + ch * 16 + i);
@@ -635,14 +725,17 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
           }
         }
       };
-      float e0[16];
+      // Up to 32 rows' exponents stay in registers; of 64 rows the first 16's do, and the
+      // others' are formed again below.
+      constexpr int kKeep = CH <= 2 ? CH : 1;
+      float e[kKeep][16];
       float top = -INFINITY;
       if (!failed) {
 #pragma unroll
-        for (int ch = CH - 1; ch >= 0; --ch) {   // the first rows' exponents stay in registers
-          exponents(ch, lv, true, e0);
+        for (int ch = CH - 1; ch >= 0; --ch) {
+          exponents(ch, lv, true, e[ch % kKeep]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) top = fmaxf(top, e0[i]);
+          for (int i = 0; i < 16; i += 2) top = max3f(top, e[ch % kKeep][i], e[ch % kKeep][i + 1]);
         }
       }
       if (bar_or(wg_bar, kWg, failed || top > kTop + kGrow)) {
@@ -684,19 +777,23 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
             l[r] *= f[i];
           }
           if (any && any_pv) {
-            uint32_t o[16];
-            const uint32_t at = lane_addr + L::kOCol + wg * NR + ch * 16;
-            tmem_load_16cols(at, o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i]);
-            tmem_store_16cols(at, o);
+            for (int term = 0; term < (L::kWide ? 3 : 1); ++term) {
+              uint32_t o[16];
+              const uint32_t at = lane_addr + L::kOCol + wg * L::kOCols + term * NR + ch * 16;
+              tmem_load_16cols(at, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i]);
+              tmem_store_16cols(at, o);
+            }
           }
         }
         tmem_store_wait();
         bar_or(wg_bar, kWg, false);   // every thread has read the old maxima
         if (key < NR) negm[key] = mine_new;
         bar_or(wg_bar, kWg, false);
-        exponents(0, lv, true, e0);
+#pragma unroll
+        for (int ch = kKeep - 1; ch >= 0; --ch) exponents(ch, lv, true, e[ch]);
       }
       // Weights, their sum, and their three E5M2 terms: a weight in fp16 (11 significant
       // bits), whose upper byte is an E5M2 number; what that leaves, likewise; the last
@@ -704,7 +801,8 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       const uint32_t p_addr = sbase + L::kPOff + wg * L::kPBuf + key * 16;
 #pragma unroll
       for (int ch = 0; ch < CH; ++ch) {
-        if (ch > 0) exponents(ch, lv, true, e0);
+        if (ch >= kKeep) exponents(ch, lv, true, e[ch % kKeep]);
+        const float(&e0)[16] = e[ch % kKeep];
         uint32_t t1[8], t2[8], t3[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -739,7 +837,10 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       fence_proxy_async_smem();
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kPFull + wg));
+      if (lane == 0) {
+        mbar_arrive(bar(L::kPFull + wg));
+        mbar_arrive(bar(L::kSFree + (gi & 3)));
+      }
       any_pv = true;
       ks = ks_next;
       vs = vs_next;
@@ -753,12 +854,23 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       failed = !w.wait_warp(bar(L::kPVDone + wg), last & 1, code | (L::kPVDone + wg));
     }
     if (!failed) {
+      // Sixteen sums over 32 lanes: each step halves the rows a lane carries.
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        float v = l[r];
+      for (int ch = 0; ch < CH; ++ch) {
+        float v[16];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == (r & 31)) lsum_all[(wg * 4 + warp) * NR + r] = v;
+        for (int i = 0; i < 16; ++i) v[i] = l[ch * 16 + i];
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+          const bool up = lane & o;
+#pragma unroll
+          for (int i = 0; i < o; ++i) {
+            const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+        }
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+        if (lane < 16) lsum_all[(wg * 4 + warp) * NR + ch * 16 + lane] = v[0];
       }
     }
     if (lane == 0) mbar_arrive(bar(L::kQEmpty + qbuf));  // this warp has read the row factors
@@ -797,8 +909,19 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       uint32_t a[16], b[16];
       // 16 columns even where 8 are used: the columns behind belong to the other half.
       const int col = NR == 16 ? 0 : c0;
-      if (has0) tmem_load_16cols(lane_addr + L::kOCol + col, a);
-      if (has1) tmem_load_16cols(lane_addr + L::kOCol + NR + col, b);
+      auto load_o = [&](int g2, uint32_t (&o)[16]) {
+        const uint32_t at = lane_addr + L::kOCol + g2 * L::kOCols + col;
+        tmem_load_16cols(at, o);
+        if constexpr (L::kWide) {
+          uint32_t o2[16], o3[16];
+          tmem_load_2x16cols(at + NR, at + 2 * NR, o2, o3);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) + (__uint_as_float(o2[i]) + __uint_as_float(o3[i])));
+        }
+      };
+      if (has0) load_o(0, a);
+      if (has1) load_o(1, b);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int r = col + i;
@@ -814,6 +937,7 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(L::kOFree));
+    if (S > 1) merge_if_last();
     g += n;
     ++items;
   }
@@ -841,17 +965,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode8_kernel(const __grid_
       mbar_init(bar(L::kKVFull + s), 1);
       mbar_init(bar(L::kKVEmpty + s), 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(bar(L::kSFull + i), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(L::kSFull + i), 1);
+      mbar_init(bar(L::kSFree + i), 4);
+    }
     mbar_init(bar(L::kOFree), 8);
     mbar_init(bar(L::kFin), 1);
+    mbar_init(bar(L::kFin + 1), 1);
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(bar(L::kItemFull + i), 1);
-      mbar_init(bar(L::kItemEmpty + i), 11);  // every role but the K loader
+      mbar_init(bar(L::kItemEmpty + i), 11);  // every warp but the K loader
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kPvWarp) {
     tmem_alloc(smem_addr(const_cast<uint32_t*>(tmem_slot)), L::kTmemCols);
     tmem_relinquish();
   }
@@ -869,15 +997,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode8_kernel(const __grid_
   } else if (warp == kVWarp) {
     const uint32_t gt = loader8<D, NR, true>(p, sbase, smem, w);
     if ((threadIdx.x & 31) == 0) loaded[1] = gt;
-  } else if (warp == kMmaWarp) {
-    mma_role8<D, NR>(p, sbase, smem, tmem, w);
+  } else if (warp == kPvWarp) {
+    pv_role8<D, NR>(p, sbase, smem, tmem, w);
   } else {
-    q_role8<D, NR>(p, sbase, smem, w);
+    s_role8<D, NR>(p, sbase, smem, tmem, w);
   }
   tc_fence_before_sync();
   __syncthreads();
   if (threadIdx.x == kKWarp * 32) drain_ring8<L>(sbase, w, loaded[0], loaded[1]);
-  if (warp == kMmaWarp) {
+  if (warp == kPvWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, L::kTmemCols);
   }

@@ -519,14 +519,15 @@ int attn_kv_append_debug_error(cudaStream_t stream, int* device_code);
  *                     between the sinks and the oldest window position are neither looked up nor
  *                     read. Must be 0 with the other masks
  *   workspace         device, 16-byte aligned, attn_decode_kv8_workspace_bytes(B, Hq, Hkv, Nq, d,
- *                     num_splits) bytes, with the contract of attn_decode's (first 256 bytes zero
- *                     before the first call and after each; not shared by concurrent calls)
+ *                     num_splits) bytes, with the contract of attn_decode's, but that its first
+ *                     65536 bytes are the counters that are zero before the first call and after
+ *                     each (steps of other sizes may share it; not concurrent calls)
  *   opts              wait bound and CTA count as for attn_fwd_ex; may be NULL
  *
  * Precision: the products take the codes exactly; a bf16 query row is split into two E4M3
  * terms (exact to 2^-18 of the row's largest element); scores, statistics and sums are fp32;
  * softmax weights go to the product with V as sums of three E5M2 numbers (9 significant bits,
- * one more than bf16's); weights below 2^-28 of a row's largest are dropped there (and only there).
+ * one more than bf16's); weights below 2^-26 of a row's largest are dropped there (and only there).
  * Ownership, checks, overlap rules, bounded waits and errors as attn_decode.
  */
 int attn_decode_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
