@@ -211,14 +211,6 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float s, float inv
   for (int i = 0; i < 8; ++i) y[i] = pow2 ? x[i] * inv : __fdiv_rn(x[i], s);
   return make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
 }
-__device__ __forceinline__ float e4m3_value(uint32_t code) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(code & 0xffu));
-  float f;
-  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h));
-  return f;
-}
-
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_constant__ AppParams p) {
   constexpr int G = D / 16;                  // lanes of a row
@@ -354,9 +346,11 @@ __global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_c
             const uint32_t in[4] = {w.x, w.y, w.z, w.w};
             uint32_t out[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              out[i] = pack_e4m3x4(e4m3_value(in[i]) * ratio, e4m3_value(in[i] >> 8) * ratio,
-                                   e4m3_value(in[i] >> 16) * ratio, e4m3_value(in[i] >> 24) * ratio);
+            for (int i = 0; i < 4; ++i) {
+              float x0, x1, x2, x3;
+              e4m3x4_values(in[i], x0, x1, x2, x3);
+              out[i] = pack_e4m3x4(x0 * ratio, x1 * ratio, x2 * ratio, x3 * ratio);
+            }
             *at = make_uint4(out[0], out[1], out[2], out[3]);
           }
         }

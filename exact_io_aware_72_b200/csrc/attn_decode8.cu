@@ -26,7 +26,7 @@ namespace {
 constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxSplits = 4096;
-constexpr int64_t kMaxRows = 64;  // query rows of a work item
+constexpr int64_t kMaxRows = 32;  // query rows of a work item
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -79,8 +79,7 @@ int dec8_device_setup(Dec8Device& out) {
       void* addr = nullptr;
       if (cudaGetSymbolAddress(&addr, g_attn_dec8_error) != cudaSuccess) return ATTN_ERR_CUDA;
       info.err_word = static_cast<int*>(addr);
-      if (!set_smem<64, 16>() || !set_smem<64, 32>() || !set_smem<64, 64>() || !set_smem<128, 16>() ||
-          !set_smem<128, 32>() || !set_smem<128, 64>())
+      if (!set_smem<64, 16>() || !set_smem<64, 32>() || !set_smem<128, 16>() || !set_smem<128, 32>())
         return ATTN_ERR_CUDA;
     }
     info.probed = true;
@@ -126,10 +125,8 @@ cudaError_t launch(const Dec8Params& p, int grid, cudaStream_t stream) {
 }
 template <int D>
 cudaError_t launch_rows(const Dec8Params& p, int grid, cudaStream_t stream) {
-  // The narrowest product that holds an item's rows.
-  if (p.rows_chunk <= 16) return launch<D, 16>(p, grid, stream);
-  if (p.rows_chunk <= 32) return launch<D, 32>(p, grid, stream);
-  return launch<D, 64>(p, grid, stream);
+  // The narrower product that holds an item's rows.
+  return p.rows_chunk <= 16 ? launch<D, 16>(p, grid, stream) : launch<D, 32>(p, grid, stream);
 }
 
 }  // namespace
@@ -162,10 +159,11 @@ extern "C" int64_t attn_decode_kv8_num_splits(int64_t B, int64_t Hq, int64_t Hkv
   int64_t tiles = (max_seq_len + kKeys - 1) / kKeys + 1;
   if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window < max_seq_len)
     tiles = std::min(tiles, (window + Nq - 1 + kKeys - 1) / kKeys + 1 + (std::min(sinks, max_seq_len) + kKeys - 1) / kKeys);
-  // As for the bf16 cache: one wave of items for a batch below the SM count, otherwise items
+  // As for the bf16 cache: one wave of items for a batch below the CTA count, otherwise items
   // of at most kMaxItemTiles tiles from the shared counter; no split under four tiles.
   constexpr int64_t kMaxItemTiles = 64;
-  const int64_t s = units < sms ? sms / units : (tiles + kMaxItemTiles - 1) / kMaxItemTiles;
+  const int64_t ctas = kCtasPerSm * static_cast<int64_t>(sms);
+  const int64_t s = units < ctas ? ctas / units : (tiles + kMaxItemTiles - 1) / kMaxItemTiles;
   return std::max<int64_t>(1, std::min<int64_t>({s, std::max<int64_t>(1, tiles / 4), kMaxSplits}));
 }
 
@@ -284,7 +282,7 @@ extern "C" int attn_decode_kv8(const void* q, const void* k_cache, const void* v
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = (opts && opts->wait_timeout_ns) ? opts->wait_timeout_ns : kDefaultTimeoutNs;
 
-  int grid = static_cast<int>(std::min<int64_t>(items, dev.sm_count));
+  int grid = static_cast<int>(std::min<int64_t>(items, kCtasPerSm * dev.sm_count));
   if (opts && opts->grid_ctas > 0) grid = std::min(grid, opts->grid_ctas);
   if ((d == 64 ? launch_rows<64>(p, grid, stream) : launch_rows<128>(p, grid, stream)) != cudaSuccess)
     return ATTN_ERR_CUDA;

@@ -28,21 +28,29 @@
 //   and a weight is lost only below 2^-26 of the largest.
 // * Sums l and all statistics are fp32; out is rounded once to bf16.
 //
-// Work items, splits and the item counter are the bf16 decoding kernel's.  Two softmax
-// warpgroups take the tiles of an item in turn, each with its own m, l and O, merged at the
-// item's end.  m is per row and warpgroup: a vote over the warpgroup (one hardware barrier
-// with a reduction) finds the rare tiles where some row's maximum grew by more than 2^6.
+// Work items, splits and the item counter are the bf16 decoding kernel's.  Two CTAs share an
+// SM, each with its own items, ring and softmax warpgroup: at an item's ends (its first page
+// entries and scales, the last product, the merge) one CTA's chain of latencies, some 5 us,
+// runs under the other's tiles.  (One CTA whose two warpgroups took the tiles of an item in
+// turn stopped for it: 9 us for each item, 70 us instead of 58 for a batch of windows.)
+// m is per row: a vote over the warpgroup (one hardware barrier with a reduction) finds the
+// rare tiles where some row's maximum grew by more than 2^6.
 //
 // The splits of one (sequence, KV head, row chunk) count themselves in the workspace as they
 // finish, and the CTA that finishes the last one merges their partial results, in the order
 // of the splits (a merge launch of its own took 9 us behind a 70 us step).
 //
-// Warps: 0-3 and 4-7 softmax, 8 loads K (and fetches items), 9 loads V, 10 issues the P V
-// products, 11 prepares Q and issues the S products up to four tiles ahead.  (One issuing
-// warp spent 1500 cycles per tile on waits and issue latencies of both products, whose
-// execution takes 340; HBM delivers a tile per 1400.)  TMEM: four S buffers, then the two
-// O.  All mbarrier waits are bounded; the warpgroup barriers are reached by every warp
-// whether or not a wait gave up, and carry that news, so the roles leave together.
+// Warps: 0-3 softmax, 4 loads K (and fetches items), 5 loads V, 6 issues the P V products, 7
+// prepares Q and issues the S products ahead.  (One issuing warp spent 1500 cycles per tile
+// on waits and issue latencies of both products, whose execution takes 340; HBM delivers a
+// tile per 1400.)  TMEM: the S buffers, then O.  All mbarrier waits are bounded; the
+// warpgroup's barriers are reached by every warp whether or not a wait gave up, and carry
+// that news, so the roles leave together.
+//
+// The code is kept small: what is not in the tile loop is a call or a rolled loop, items are
+// decoded once (by the K loader) and read from shared memory.  With everything inlined the
+// kernel was 130 KB, and each item's start and end ran at the speed of instruction fetches,
+// 10 us an item.
 #pragma once
 
 #include <cuda.h>
@@ -68,9 +76,10 @@ using attn_sm100_dec::kDRoleSoftmax;
 constexpr int kDRoleS = 4;
 
 constexpr int kKeys = 128;  // keys per tile
-constexpr int kThreads = 384;
-constexpr int kWg = 128;    // threads of a softmax warpgroup
-constexpr int kKWarp = 8, kVWarp = 9, kPvWarp = 10, kSWarp = 11;
+constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 2;
+constexpr int kWg = 128;    // threads of the softmax warpgroup
+constexpr int kKWarp = 4, kVWarp = 5, kPvWarp = 6, kSWarp = 7;
 constexpr int kItemSlots = 4;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTop = 9.f;      // weights at the running maximum are 2^kTop
@@ -106,75 +115,82 @@ struct Dec8Params {
 template <int D, int NR>
 struct Smem8 {
   static_assert(D == 64 || D == 128, "head dim");
-  static_assert(NR == 16 || NR == 32 || NR == 64, "query rows");
+  static_assert(NR == 16 || NR == 32, "query rows");
   static constexpr uint32_t kTileBytes = kKeys * D;
   static constexpr uint32_t kQTerm = NR * D, kQBuf = 2 * kQTerm;     // two E4M3 terms
   static constexpr uint32_t kPTerm = NR * kKeys, kPBuf = 3 * kPTerm; // three E5M2 terms
-  static constexpr uint32_t kSmall = 8192;                            // arrays and barriers below
-  static constexpr uint32_t kRoom = 232448 - 1024 - kSmall - 2 * kQBuf - 2 * kPBuf;
-  static constexpr int kStages = static_cast<int>(kRoom / kTileBytes) / 2 * 2 < 20
-                                     ? static_cast<int>(kRoom / kTileBytes) / 2 * 2
-                                     : 20;
-  static constexpr uint32_t kRingOff = 0;
-  static constexpr uint32_t kQOff = kStages * kTileBytes;
+  static constexpr uint32_t kAlloc = 115712;                         // half of an SM's shared memory
+  static constexpr uint32_t kSmall = 2304;                           // arrays and barriers below
+  static constexpr int kSlots = static_cast<int>((kAlloc - 1024 - kSmall - 2 * kQBuf - kPBuf) / kTileBytes);
+  // Separate rings for K and V: each is waited on by one loader, in order, so a slot's phases
+  // cannot be mistaken (on one ring of odd length, K and V would take turns on a slot and a
+  // parity wait could pass two phases early).  V slots are held longer.
+  static constexpr int kKSlots = kSlots / 2 < 6 ? kSlots / 2 : 6;
+  static constexpr int kVSlots = (kSlots + 1) / 2 < 6 ? (kSlots + 1) / 2 : 6;
+  static constexpr int kSBufs = NR == 16 ? 4 : 2;
+  static constexpr uint32_t kKOff = 0;
+  static constexpr uint32_t kVOff = kKSlots * kTileBytes;
+  static constexpr uint32_t kQOff = kVOff + kVSlots * kTileBytes;
   static constexpr uint32_t kPOff = kQOff + 2 * kQBuf;
-  static constexpr uint32_t kFrOff = kPOff + 2 * kPBuf;         // [2 Q buffers][NR] row factors
-  static constexpr uint32_t kNegMOff = kFrOff + 2 * NR * 4;     // [2 warpgroups][NR] kTop - m
-  static constexpr uint32_t kHiOff = kNegMOff + 2 * NR * 4;     // [2][NR] last visible position
-  static constexpr uint32_t kLoOff = kHiOff + 2 * NR * 4;       // [2][NR] first position of the window
-  static constexpr uint32_t kWmaxOff = kLoOff + 2 * NR * 4;     // [2][4 warps][NR]
-  static constexpr uint32_t kLsumOff = kWmaxOff + 8 * NR * 4;   // [2][4 warps][NR]
-  static constexpr uint32_t kCoefOff = kLsumOff + 8 * NR * 4;   // [2][NR] weight of a warpgroup's O
-  static constexpr uint32_t kBarOff = kCoefOff + 2 * NR * 4;
+  static constexpr uint32_t kFrOff = kPOff + kPBuf;             // [2 Q buffers][NR] row factors
+  static constexpr uint32_t kNegMOff = kFrOff + 2 * NR * 4;     // [2][NR] kTop - m, the buffers in turn
+  static constexpr uint32_t kHiOff = kNegMOff + 2 * NR * 4;     // [NR] last visible position
+  static constexpr uint32_t kLoOff = kHiOff + NR * 4;           // [NR] first position of the window
+  static constexpr uint32_t kWmaxOff = kLoOff + NR * 4;         // [4 warps][NR]; at an item's end its sums
+  static constexpr uint32_t kCoefOff = kWmaxOff + 4 * NR * 4;   // [NR] 1 / sum
+  static constexpr uint32_t kBarOff = kCoefOff + NR * 4;
   static constexpr int kQFull = 0;                     // x2
   static constexpr int kQEmpty = 2;                    // x2
-  static constexpr int kKVFull = 4;
-  static constexpr int kKVEmpty = kKVFull + kStages;
-  static constexpr int kSFull = kKVEmpty + kStages;    // x4
-  static constexpr int kSFree = kSFull + 4;            // x4
-  static constexpr int kPFull = kSFree + 4;            // x2, one per warpgroup
-  static constexpr int kPVDone = kPFull + 2;           // x2
-  static constexpr int kOFree = kPVDone + 2;
+  static constexpr int kKFull = 4;                     // x kKSlots
+  static constexpr int kKEmpty = kKFull + kKSlots;
+  static constexpr int kVFull = kKEmpty + kKSlots;     // x kVSlots
+  static constexpr int kVEmpty = kVFull + kVSlots;
+  static constexpr int kSFull = kVEmpty + kVSlots;     // x kSBufs
+  static constexpr int kSFree = kSFull + kSBufs;       // x kSBufs
+  static constexpr int kPFull = kSFree + kSBufs;
+  static constexpr int kPVDone = kPFull + 1;
+  static constexpr int kOFree = kPVDone + 1;
   static constexpr int kFin = kOFree + 1;              // x2, one per issuing warp
   static constexpr int kItemFull = kFin + 2;
   static constexpr int kItemEmpty = kItemFull + kItemSlots;
   static constexpr int kNumBars = kItemEmpty + kItemSlots;
-  static constexpr uint32_t kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr uint32_t kItemOff = kMiscOff + 16;
-  static constexpr uint32_t kBytes = kItemOff + 4 * kItemSlots;
-  static constexpr uint32_t kAlloc = 232448;
-  static_assert(kBytes - kFrOff <= kSmall && kBytes + 1024 <= kAlloc, "shared memory per CTA");
-  // The terms of Q and of P are side by side in one product's N where TMEM has room for
-  // their separate sums (a product of few rows takes the time of reading its A operand, 128
-  // rows, whatever N is), and further products into the same sums otherwise.
-  static constexpr bool kWide = NR <= 32;
-  static constexpr uint32_t kSCols = kWide ? 2 * NR : NR, kOCols = kWide ? 3 * NR : NR;
-  static constexpr uint32_t kSCol = 0, kOCol = 4 * kSCols;      // + kSCols per buffer, kOCols per warpgroup
-  static constexpr uint32_t kTmemCols = NR == 16 ? 256 : 512;
-  static_assert(4 * kSCols + 2 * kOCols <= kTmemCols, "TMEM columns");
+  static constexpr uint32_t kItemOff = (kBarOff + kNumBars * 8 + 15) / 16 * 16;  // kItemSlots items of 64 bytes
+  static constexpr uint32_t kMiscOff = kItemOff + 64 * kItemSlots;
+  static constexpr uint32_t kBytes = kMiscOff + 16;
+  static_assert(kKSlots >= 2 && kBytes - kFrOff <= kSmall && kBytes + 1024 <= kAlloc, "shared memory per CTA");
+  // The terms of Q and of P lie side by side in one product's N, with separate sums: a product
+  // of few rows takes the time of reading its A operand, 128 rows, whatever N is.
+  static constexpr uint32_t kSCols = 2 * NR, kOCols = 3 * NR;
+  static constexpr uint32_t kSCol = 0, kOCol = kSBufs * kSCols;
+  static constexpr uint32_t kTmemCols = 256;                    // two CTAs share 512
+  static_assert(kOCol + kOCols <= kTmemCols, "TMEM columns");
 };
 
 // ------------------------------------------------------------ work items
 // Tiles of a sequence are numbered u = 0, 1, ... over what the step can see: the ns tiles
 // that hold sinks before the window's first tile, then the window's.  tile(u) is the
 // position range's tile.
-struct Item8 {
-  int b, hkv, s;
+struct __align__(16) Item8 {
+  int idx;               // its number; -2: no more items
+  int b, hkv, s, unit;   // unit: number of the (b, KV head, row chunk)
   int L, lo_pos, sinks;  // cached positions; oldest position in any row's window; sinks
   int ns, first;         // tile(u) = u < ns ? u : u - ns + first
   int t0, t1;            // range of u of this split (empty when t1 < t0)
   int row0, rows;
-  bool bad;
+  int bad, pad;
   __device__ __forceinline__ int tile(int u) const { return u < ns ? u : u - ns + first; }
   __device__ __forceinline__ bool seen(int pos) const { return pos < L && (pos >= lo_pos || pos < sinks); }
 };
 
 __device__ __forceinline__ Item8 item8(const Dec8Params& p, int idx) {
   Item8 it;
-  it.s = idx % p.num_splits;
-  idx /= p.num_splits;
+  it.idx = idx;
+  // Row chunks of one split are neighbours: they run together and share its keys in L2.
   const int rc = idx % p.row_chunks;
   idx /= p.row_chunks;
+  it.s = idx % p.num_splits;
+  idx /= p.num_splits;
+  it.unit = idx * p.row_chunks + rc;
   it.hkv = idx % p.Hkv;
   it.b = idx / p.Hkv;
   it.L = __ldg(p.seq_lens + it.b);
@@ -184,6 +200,7 @@ __device__ __forceinline__ Item8 item8(const Dec8Params& p, int idx) {
   it.lo_pos = it.ns = it.first = it.t0 = 0;
   it.sinks = 0;
   it.t1 = -1;
+  it.pad = 0;
   if (!it.bad && it.L > 0) {
     if (p.mask_kind == kDMaskWindow) {
       it.lo_pos = max(0, it.L - p.Nq - p.window + 1);
@@ -199,17 +216,37 @@ __device__ __forceinline__ Item8 item8(const Dec8Params& p, int idx) {
   return it;
 }
 
+// A bounded wait whose rarely needed part is a call.
+__device__ __noinline__ bool wait_long8(uint32_t bar, uint32_t parity, int code, const DecWaiter* w) {
+  return w->wait(bar, parity, code);
+}
+struct Waiter8 {
+  const DecWaiter* w;
+  __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int code) const {
+    bool got = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, got)) got = got || wait_long8(bar, parity, code, w);
+    return __all_sync(0xffffffffu, got);
+  }
+};
+
+// The next item for a consuming warp; idx -2: no more, -1: the wait gave up.
 template <class L>
-__device__ __forceinline__ int take_item8(uint32_t sbase, const uint8_t* smem, const DecWaiter& w, uint32_t& k,
-                                          int code) {
+__device__ __forceinline__ Item8 take_item8(uint32_t sbase, const uint8_t* smem, const Waiter8& w, uint32_t& k,
+                                            int code) {
   const uint32_t slot = k % kItemSlots;
   const uint32_t full = sbase + L::kBarOff + 8u * (L::kItemFull + slot);
-  if (!w.wait_warp(full, (k / kItemSlots) & 1, code | (L::kItemFull + slot))) return -1;
-  const int idx = *reinterpret_cast<const volatile int*>(smem + L::kItemOff + 4 * slot);
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(sbase + L::kBarOff + 8u * (L::kItemEmpty + slot));
-  ++k;
-  return idx;
+  Item8 it;
+  if (w.wait_warp(full, (k / kItemSlots) & 1, code | (L::kItemFull + slot))) {
+    it = *reinterpret_cast<const Item8*>(smem + L::kItemOff + sizeof(Item8) * slot);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(sbase + L::kBarOff + 8u * (L::kItemEmpty + slot));
+    ++k;
+  } else {
+    it.idx = -1;
+    it.t0 = 0;
+    it.t1 = -1;
+  }
+  return it;
 }
 
 // ------------------------------------------------------------ small pieces
@@ -247,10 +284,6 @@ __device__ __forceinline__ void tmem_load_2x16cols(uint32_t ta, uint32_t tb, uin
       : "r"(ta), "r"(tb)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_3d_first(uint32_t dst, const CUtensorMap* map, uint32_t bar, int y, int z,
-                                                  uint64_t policy) {
-  tma_load_3d(dst, map, bar, 0, y, z, policy);
-}
 // Shared-memory descriptors: swizzle by the row's bytes (128: layout 2, 64: layout 4), or none.
 __device__ __forceinline__ uint64_t desc8(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
@@ -274,181 +307,196 @@ __device__ __forceinline__ int ordered(float x) {  // order-preserving, its own 
 __device__ __forceinline__ float unordered(int b) { return __int_as_float(b ^ ((b >> 31) & 0x7fffffff)); }
 
 // ------------------------------------------------------------ loaders
-// As in the bf16 kernel: K of the CTA's g-th tile goes to ring index 2g, V to 2g + 1; lane i
-// copies the i-th box of the tile; page-table entries are read two tiles ahead.
-template <int D, int NR, bool kV>
-__device__ __forceinline__ uint32_t loader8(const Dec8Params& p, uint32_t sbase, uint8_t* smem, const DecWaiter& w) {
+// One warp for K and one for V, on rings of their own; lane i copies the i-th box of a tile.
+// Page-table entries are read two tiles ahead.  The K warp also fetches the items, one ahead
+// of the one it loads, and publishes them.
+template <int D, int NR>
+__device__ __forceinline__ uint32_t loader8(const Dec8Params& p, uint32_t sbase, uint8_t* smem, const Waiter8& w,
+                                            bool kv) {
   using L = Smem8<D, NR>;
   auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
   const int lane = threadIdx.x & 31;
-  const uint64_t pol = l2_policy_evict_first();
-  const CUtensorMap* map = kV ? &p.tm_v : &p.tm_k;
+  // Every cached byte is read once per step, or once per row chunk.
+  const uint64_t pol = p.row_chunks == 1 ? l2_policy_evict_first() : l2_policy_evict_last();
+  const CUtensorMap* map = kv ? &p.tm_v : &p.tm_k;
+  const uint32_t slots = kv ? L::kVSlots : L::kKSlots;
+  const uint32_t ring = sbase + (kv ? L::kVOff : L::kKOff) + lane * p.rows_per_load * D;
+  const int full = kv ? L::kVFull : L::kKFull, empty = kv ? L::kVEmpty : L::kKEmpty;
   if (lane == 0) tma_prefetch_map(map);
   const int code = kDRoleLoader << 8;
-  uint32_t gt = 0, k_item = 0;
+  uint32_t gt = 0, k_item = 0, slot = 0, round = 0;  // tile gt goes to `slot`, filled `round` times before
   int next = 0;
-  if (!kV && lane == 0) next = static_cast<int>(atomicAdd(p.sched, 1u));
-  bool ok = true;
-  while (ok) {
-    int idx;
-    if constexpr (kV) {
-      idx = take_item8<L>(sbase, smem, w, k_item, code);
-      if (idx < 0) break;
+  auto fetch = [&]() {
+    if (lane == 0) next = static_cast<int>(atomicAdd(p.sched, 1u));
+  };
+  // Decodes and publishes the fetched item (or the end), and fetches another.
+  auto publish = [&](Item8& it) -> bool {
+    const uint32_t s = k_item % kItemSlots;
+    if (k_item >= kItemSlots &&
+        !w.wait_warp(bar(L::kItemEmpty + s), (k_item / kItemSlots - 1) & 1, code | (L::kItemEmpty + s)))
+      return false;
+    const int idx = __shfl_sync(0xffffffffu, next, 0);
+    if (idx < p.num_items) {
+      fetch();
+      it = item8(p, idx);
     } else {
-      const uint32_t slot_i = k_item % kItemSlots;
-      if (k_item >= (uint32_t)kItemSlots &&
-          !w.wait_warp(bar(L::kItemEmpty + slot_i), ((k_item / kItemSlots) - 1) & 1, code | (L::kItemEmpty + slot_i)))
-        break;
-      idx = __shfl_sync(0xffffffffu, next, 0);
-      if (lane == 0) {
-        *reinterpret_cast<volatile int*>(smem + L::kItemOff + 4 * slot_i) = idx < p.num_items ? idx : -2;
-        mbar_arrive(bar(L::kItemFull + slot_i));
-      }
-      ++k_item;
-      if (idx >= p.num_items) break;
-      if (lane == 0) next = static_cast<int>(atomicAdd(p.sched, 1u));
+      it.idx = -2;
+      it.t0 = 0;
+      it.t1 = -1;
     }
-    const Item8 it = item8(p, idx);
-    if (it.t1 < it.t0) continue;
-    const int* trow = p.block_table + static_cast<size_t>(it.b) * p.max_pages;
+    if (lane == 0) {
+      *reinterpret_cast<Item8*>(smem + L::kItemOff + sizeof(Item8) * s) = it;
+      mbar_arrive(bar(L::kItemFull + s));
+    }
+    __syncwarp();
+    ++k_item;
+    return true;
+  };
+  Item8 it, nx;
+  if (!kv) {
+    fetch();
+    if (!publish(it)) return 0;
+  }
+  while (true) {
+    if (kv) {
+      it = take_item8<L>(sbase, smem, w, k_item, code);
+    }
+    if (it.idx < 0) break;
+    if (!kv && !publish(nx)) break;
     // First position of this lane's box in tile u, or -1 when the box holds nothing the step sees.
     auto box_pos = [&](int u) -> int {
       if (u > it.t1 || lane >= p.loads_per_tile) return -1;
       const int pos0 = it.tile(u) * kKeys + lane * p.rows_per_load;
       return (pos0 >= it.L || (pos0 + p.rows_per_load <= it.lo_pos && pos0 >= it.sinks)) ? -1 : pos0;
     };
+    const int* trow = p.block_table + static_cast<size_t>(it.b) * p.max_pages;
     auto entry = [&](int pos0) -> int { return pos0 < 0 ? 0 : __ldg(trow + (pos0 >> p.page_shift)); };
-    int p0 = box_pos(it.t0), p1 = box_pos(it.t0 + 1);
-    int e0 = entry(p0), e1 = entry(p1);
-    for (int u = it.t0; u <= it.t1; ++u) {
-      const int p2 = box_pos(u + 2), e2 = entry(p2);
+    bool ok = true;
+    int p0 = -1, p1 = -1, e0 = 0, e1 = 0;
+#pragma unroll 1
+    for (int u = it.t0 - 2; u <= it.t1; ++u) {   // two rounds ahead to fill the entries
       int page = e0;
       if (p0 >= 0 && (page < 0 || page >= p.num_pages)) {
         atomicCAS(p.err, 0, kDErrPage | (it.b & 0xFFFFF));
         page = 0;  // a stand-in inside the pool; the step's result is then undefined
       }
-      const uint32_t ring_idx = 2 * gt + (kV ? 1 : 0), slot = ring_idx % L::kStages;
-      if (ring_idx >= (uint32_t)L::kStages &&
-          !w.wait_warp(bar(L::kKVEmpty + slot), ((ring_idx / L::kStages) - 1) & 1, code | (L::kKVEmpty + slot))) {
+      const int z = page * p.Hkv + it.hkv, at = p0;
+      asm volatile("" ::"r"(z) : "memory");  // this entry is used before a later one is asked for
+      p0 = p1;
+      e0 = e1;
+      p1 = box_pos(u + 2);
+      e1 = entry(p1);
+      if (u < it.t0) continue;
+      if (round > 0 && !w.wait_warp(bar(empty + slot), (round - 1) & 1, code | (empty + slot))) {
         ok = false;
         break;
       }
-      const unsigned boxes = __ballot_sync(0xffffffffu, p0 >= 0);
+      const unsigned boxes = __ballot_sync(0xffffffffu, at >= 0);
       if (lane == 0)
-        mbar_arrive_expect_tx(bar(L::kKVFull + slot), __popc(boxes) * static_cast<uint32_t>(p.rows_per_load) * D);
+        mbar_arrive_expect_tx(bar(full + slot), __popc(boxes) * static_cast<uint32_t>(p.rows_per_load) * D);
       __syncwarp();
-      if (p0 >= 0)
-        tma_load_3d_first(sbase + L::kRingOff + slot * L::kTileBytes + lane * p.rows_per_load * D, map,
-                          bar(L::kKVFull + slot), p0 & (p.page_size - 1), page * p.Hkv + it.hkv, pol);
+      if (at >= 0) tma_load_3d(ring + slot * L::kTileBytes, map, bar(full + slot), 0, at & (p.page_size - 1), z, pol);
       ++gt;
-      p0 = p1;
-      e0 = e1;
-      p1 = p2;
-      e1 = e2;
+      if (++slot == slots) {
+        slot = 0;
+        ++round;
+      }
     }
+    if (!ok) break;
+    if (!kv) it = nx;
   }
   return gt;
 }
 
-template <class L>
-__device__ __forceinline__ void drain_ring8(uint32_t sbase, const DecWaiter& w, uint32_t gt_k, uint32_t gt_v) {
-  for (uint32_t s = 0; s < (uint32_t)L::kStages; ++s) {
-    // an even ring: even slots hold K, odd slots V
-    const uint32_t gt = (s & 1) ? gt_v : gt_k, lead = s >> 1, half = L::kStages / 2;
-    if (gt > lead) {
-      const uint32_t fills = (gt - 1 - lead) / half;  // completed refills of the slot's last load
-      w.drain(sbase + L::kBarOff + 8u * (L::kKVFull + s), fills & 1, (kDRoleLoader << 8) | (L::kKVFull + s));
-    }
-  }
+// Every copy must land before the CTA exits: a slot is loaded again only after its load
+// landed and was read, so each slot's last load is waited for.
+__device__ __forceinline__ void drain_ring8(uint32_t full, int slots, const DecWaiter& w, uint32_t gt) {
+  for (uint32_t s = 0; s < static_cast<uint32_t>(slots) && s < gt; ++s)
+    w.drain(full + 8u * s, ((gt - 1 - s) / slots) & 1, (kDRoleLoader << 8) | s);
 }
 
 // ------------------------------------------------------------ Q
 // One warp: each row of an item becomes two E4M3 terms in shared memory (K-major, in the
-// swizzle of a D-byte row), with its factor scale log2(e) / (the row's power of two).
+// swizzle of a D-byte row), with its factor 1 / (the row's power of two).
 template <int D, int NR>
 __device__ __forceinline__ void prepare_q8(const Dec8Params& p, const Item8& it, uint8_t* smem, uint32_t buf) {
   using L = Smem8<D, NR>;
-  const int lane = threadIdx.x & 31;
-  const size_t row = (static_cast<size_t>(it.b) * p.Hq + static_cast<size_t>(it.hkv) * p.group) * p.Nq + it.row0;
-  const __nv_bfloat16* src = p.q + row * D;
+  constexpr int G = D / 16;          // lanes of a row, 16 elements each
+  constexpr int kRows = 32 / G;      // rows of a pass
+  constexpr int kBatch = 2;          // passes whose loads are in flight together
+  const int lane = threadIdx.x & 31, c = lane % G;
+  const size_t row0 = (static_cast<size_t>(it.b) * p.Hq + static_cast<size_t>(it.hkv) * p.group) * p.Nq + it.row0;
+  const uint4* src = reinterpret_cast<const uint4*>(p.q + row0 * D) + 2 * c;
   float* fr = reinterpret_cast<float*>(smem + L::kFrOff) + buf * NR;
   uint8_t* q1 = smem + L::kQOff + buf * L::kQBuf;
-  constexpr int E = D / 32;  // elements of a lane
-#pragma unroll 8
-  for (int r = 0; r < NR; ++r) {
-    float x[E];
+#pragma unroll 1
+  for (int b = 0; b < NR; b += kRows * kBatch) {
+    uint4 raw[kBatch][2];
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = 0.f;
-    if (r < it.rows) {
-      const uint32_t* s32 = reinterpret_cast<const uint32_t*>(src + static_cast<size_t>(r) * D) + lane * (E / 2);
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = b + k * kRows + lane / G;
+      const bool live = r < it.rows;
+      raw[k][0] = live ? __ldg(src + static_cast<size_t>(r) * (D / 8)) : make_uint4(0u, 0u, 0u, 0u);
+      raw[k][1] = live ? __ldg(src + static_cast<size_t>(r) * (D / 8) + 1) : make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        const uint32_t v = __ldg(s32 + i);
-        x[2 * i] = __uint_as_float(v << 16);
-        x[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = b + k * kRows + lane / G;
+      const uint32_t w[8] = {raw[k][0].x, raw[k][0].y, raw[k][0].z, raw[k][0].w,
+                             raw[k][1].x, raw[k][1].y, raw[k][1].z, raw[k][1].w};
+      uint32_t big = 0;  // largest magnitude, bf16 bits in each half
+#pragma unroll
+      for (int i = 0; i < 8; ++i) big = max_u16x2(big, w[i] & 0x7fff7fffu);
+      big = max(big >> 16, big & 0xffffu);
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+      // Multiplier 2^(7 - exponent): the row's largest lands in [128, 256).  E4M3 has no
+      // infinities: a row that holds one (or a NaN) becomes NaN.
+      const int e = min(max(134 - static_cast<int>(big >> 7), -126), 126);
+      const float mul = big >= 0x7f80u ? __int_as_float(0x7fffffff)
+                                       : (big ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 1.f);
+      uint32_t c1[4], c2[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x0 = __uint_as_float(w[2 * i] << 16) * mul, x1 = __uint_as_float(w[2 * i] & 0xffff0000u) * mul;
+        const float x2 = __uint_as_float(w[2 * i + 1] << 16) * mul;
+        const float x3 = __uint_as_float(w[2 * i + 1] & 0xffff0000u) * mul;
+        c1[i] = pack_e4m3x4(x0, x1, x2, x3);
+        float y0, y1, y2, y3;
+        e4m3x4_values(c1[i], y0, y1, y2, y3);
+        c2[i] = pack_e4m3x4(x0 - y0, x1 - y1, x2 - y2, x3 - y3);
       }
+      // 16-byte chunk c of the row, where the swizzle of D-byte rows puts it.
+      const uint32_t at = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+      *reinterpret_cast<uint4*>(q1 + at) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
+      *reinterpret_cast<uint4*>(q1 + L::kQTerm + at) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
+      if (c == 0) fr[r] = 1.f / mul;
     }
-    uint32_t big = 0;
-#pragma unroll
-    for (int i = 0; i < E; ++i) big = max(big, __float_as_uint(x[i]) & 0x7fffffffu);
-    big = __reduce_max_sync(0xffffffffu, big);
-    // Multiplier 2^(7 - exponent): the row's largest lands in [128, 256).
-    const int e = static_cast<int>(big >> 23) - 127;
-    const int mul_e = min(max(7 - e, -126), 126);
-    float mul = big ? __uint_as_float(static_cast<uint32_t>(mul_e + 127) << 23) : 1.f;
-    if (big >= 0x7f800000u) mul = __int_as_float(0x7fffffff);  // E4M3 has no infinities: the row becomes NaN
-    float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < E; ++i) hi[i] = x[i] * mul;
-    const uint32_t c1 = pack_e4m3x4(hi[0], hi[1], hi[2], hi[3]);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      uint32_t h2;
-      float f;
-      asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}"
-          : "=r"(h2)
-          : "r"((c1 >> (8 * i)) & 0xffu));
-      asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h2));
-      lo[i] = hi[i] - f;
-    }
-    const uint32_t c2 = pack_e4m3x4(lo[0], lo[1], lo[2], lo[3]);
-    if constexpr (D == 128) {
-      const uint32_t at = r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-      *reinterpret_cast<uint32_t*>(q1 + at) = c1;
-      *reinterpret_cast<uint32_t*>(q1 + L::kQTerm + at) = c2;
-    } else {
-      const uint32_t at = r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2;
-      *reinterpret_cast<uint16_t*>(q1 + at) = static_cast<uint16_t>(c1);
-      *reinterpret_cast<uint16_t*>(q1 + L::kQTerm + at) = static_cast<uint16_t>(c2);
-    }
-    if (lane == 0) fr[r] = p.scale_log2 / mul;
   }
   fence_proxy_async_smem();
   __syncwarp();
 }
 
 // ------------------------------------------------------------ products
-// S^T_j = K_j (Q1 + Q2)^T for every tile of every item, as far ahead as K, the four S buffers
-// and the two Q buffers allow.
+// S^T_j = K_j (Q1, Q2)^T for every tile of every item, as far ahead as K, the S buffers and
+// the two Q buffers allow.
 template <int D, int NR>
 __device__ __forceinline__ void s_role8(const Dec8Params& p, uint32_t sbase, uint8_t* smem, uint32_t tmem,
-                                        const DecWaiter& w) {
+                                        const Waiter8& w) {
   using L = Smem8<D, NR>;
   auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
   constexpr uint32_t kLayout = D == 128 ? 2 : 4;   // 128- or 64-byte swizzle: one row per line
   constexpr uint32_t kAtom = 8 * D;                // eight rows
   constexpr uint32_t idesc_s = idesc8(L::kSCols, 0, 0, false, false);
-  constexpr int kProducts = L::kWide ? 1 : 2;
-  const uint64_t k_desc0 = desc8(sbase + L::kRingOff, 16, kAtom, kLayout);
+  const uint64_t k_desc0 = desc8(sbase + L::kKOff, 16, kAtom, kLayout);
   const uint64_t q_desc0 = desc8(sbase + L::kQOff, 16, kAtom, kLayout);
   const bool leader = elect_one();  // issues the products, so that the commits track them
   const int code = kDRoleS << 8;
   uint32_t g = 0, items = 0, k_item = 0;
   bool ok = true;
   while (ok) {
-    const int idx = take_item8<L>(sbase, smem, w, k_item, code);
-    if (idx < 0) break;
-    const Item8 it = item8(p, idx);
+    const Item8 it = take_item8<L>(sbase, smem, w, k_item, code);
+    if (it.idx < 0) break;
     if (it.t1 < it.t0) continue;
     const int n = it.t1 - it.t0 + 1;
     const uint32_t qbuf = items & 1;
@@ -456,25 +504,24 @@ __device__ __forceinline__ void s_role8(const Dec8Params& p, uint32_t sbase, uin
     prepare_q8<D, NR>(p, it, smem, qbuf);
     if (leader) mbar_arrive(bar(L::kQFull + qbuf));
     const uint64_t qd = q_desc0 + ((qbuf * L::kQBuf) >> 4);
+#pragma unroll 1
     for (int j = 0; j < n; ++j) {
-      const uint32_t gi = g + j, ki = 2 * gi, slot = ki % L::kStages;
-      if ((gi >= 4 && !w.wait_warp(bar(L::kSFree + (gi & 3)), ((gi >> 2) - 1) & 1, code | (L::kSFree + (gi & 3)))) ||
-          !w.wait_warp(bar(L::kKVFull + slot), (ki / L::kStages) & 1, code | (L::kKVFull + slot))) {
+      const uint32_t gi = g + j, slot = gi % L::kKSlots;
+      const uint32_t sb = gi % L::kSBufs;
+      if ((gi >= L::kSBufs && !w.wait_warp(bar(L::kSFree + sb), (gi / L::kSBufs - 1) & 1, code | (L::kSFree + sb))) ||
+          !w.wait_warp(bar(L::kKFull + slot), (gi / L::kKSlots) & 1, code | (L::kKFull + slot))) {
         ok = false;
         break;
       }
       tc_fence_after_sync();
-      const uint32_t s_tmem = tmem + L::kSCol + (gi & 3) * L::kSCols;
+      const uint32_t s_tmem = tmem + L::kSCol + sb * L::kSCols;
       const uint64_t kd = k_desc0 + ((slot * L::kTileBytes) >> 4);
       if (leader) {
 #pragma unroll
-        for (int term = 0; term < kProducts; ++term)
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            mma_f8f6f4_ss(s_tmem, kd + ((kk * 32) >> 4), qd + ((term * L::kQTerm + kk * 32) >> 4), idesc_s,
-                          (term | kk) ? 1u : 0u);
-        tc_commit(bar(L::kSFull + (gi & 3)));
-        tc_commit(bar(L::kKVEmpty + slot));
+        for (int kk = 0; kk < D / 32; ++kk)
+          mma_f8f6f4_ss(s_tmem, kd + ((kk * 32) >> 4), qd + ((kk * 32) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+        tc_commit(bar(L::kSFull + sb));
+        tc_commit(bar(L::kKEmpty + slot));
         if (j == n - 1) tc_commit(bar(L::kQEmpty + qbuf));
       }
       __syncwarp();
@@ -485,21 +532,20 @@ __device__ __forceinline__ void s_role8(const Dec8Params& p, uint32_t sbase, uin
   // Every product this warp issued must complete before TMEM is freed.
   if (leader) tc_commit(bar(L::kFin));
   __syncwarp();
-  w.drain(bar(L::kFin), 0, code | L::kFin);
+  w.w->drain(bar(L::kFin), 0, code | L::kFin);
 }
 
-// O_w += V_j^T (P1 + P2 + P3), w the tile's warpgroup.
+// O += V_j^T (P1, P2, P3).
 template <int D, int NR>
 __device__ __forceinline__ void pv_role8(const Dec8Params& p, uint32_t sbase, const uint8_t* smem, uint32_t tmem,
-                                         const DecWaiter& w) {
+                                         const Waiter8& w) {
   using L = Smem8<D, NR>;
   auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
   constexpr uint32_t kLayout = D == 128 ? 2 : 4;
   constexpr uint32_t idesc_o = idesc8(L::kOCols, 0, 1, true, true);
-  constexpr int kProducts = L::kWide ? 1 : 3;
   // V^T: M runs along a row.  With d = 64 the rows end after 64, and a stride of 0 to the
   // next 64 lets lanes 64 .. 127 repeat lanes 0 .. 63.
-  const uint64_t v_desc0 = desc8(sbase + L::kRingOff, 0, 8 * D, kLayout);
+  const uint64_t v_desc0 = desc8(sbase + L::kVOff, 0, 8 * D, kLayout);
   // P: units of 16 rows, 16 bytes per key; eight keys are a core matrix.
   const uint64_t p_desc0 = desc8(sbase + L::kPOff, 128, kKeys * 16, 0);
   const bool leader = elect_one();
@@ -507,33 +553,28 @@ __device__ __forceinline__ void pv_role8(const Dec8Params& p, uint32_t sbase, co
   uint32_t g = 0, items = 0, k_item = 0;
   bool ok = true;
   while (ok) {
-    const int idx = take_item8<L>(sbase, smem, w, k_item, code);
-    if (idx < 0) break;
-    const Item8 it = item8(p, idx);
+    const Item8 it = take_item8<L>(sbase, smem, w, k_item, code);
+    if (it.idx < 0) break;
     if (it.t1 < it.t0) continue;
     const int n = it.t1 - it.t0 + 1;
+#pragma unroll 1
     for (int j = 0; j < n; ++j) {
-      const uint32_t gi = g + j, wg = gi & 1, vi = 2 * gi + 1, slot = vi % L::kStages;
-      if (!w.wait_warp(bar(L::kPFull + wg), (gi >> 1) & 1, code | (L::kPFull + wg)) ||
-          !w.wait_warp(bar(L::kKVFull + slot), (vi / L::kStages) & 1, code | (L::kKVFull + slot)) ||
+      const uint32_t gi = g + j, slot = gi % L::kVSlots;
+      if (!w.wait_warp(bar(L::kPFull), gi & 1, code | L::kPFull) ||
+          !w.wait_warp(bar(L::kVFull + slot), (gi / L::kVSlots) & 1, code | (L::kVFull + slot)) ||
           (j == 0 && items > 0 && !w.wait_warp(bar(L::kOFree), (items - 1) & 1, code | L::kOFree))) {
         ok = false;
         break;
       }
       tc_fence_after_sync();
-      const uint32_t o_tmem = tmem + L::kOCol + wg * L::kOCols;
       const uint64_t vd = v_desc0 + ((slot * L::kTileBytes) >> 4);
-      const uint64_t pd = p_desc0 + ((wg * L::kPBuf) >> 4);
-      const uint32_t more = j >= 2 ? 1u : 0u;  // each warpgroup's first tile of the item starts its O
       if (leader) {
 #pragma unroll
-        for (int term = 0; term < kProducts; ++term)
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 32; ++kk)
-            mma_f8f6f4_ss(o_tmem, vd + ((kk * 32 * D) >> 4), pd + ((term * L::kPTerm + kk * 32 * 16) >> 4), idesc_o,
-                          (term | kk) ? 1u : more);
-        tc_commit(bar(L::kPVDone + wg));
-        tc_commit(bar(L::kKVEmpty + slot));
+        for (int kk = 0; kk < kKeys / 32; ++kk)
+          mma_f8f6f4_ss(tmem + L::kOCol, vd + ((kk * 32 * D) >> 4), p_desc0 + ((kk * 32 * 16) >> 4), idesc_o,
+                        (j | kk) ? 1u : 0u);
+        tc_commit(bar(L::kPVDone));
+        tc_commit(bar(L::kVEmpty + slot));
       }
       __syncwarp();
     }
@@ -542,113 +583,116 @@ __device__ __forceinline__ void pv_role8(const Dec8Params& p, uint32_t sbase, co
   }
   if (leader) tc_commit(bar(L::kFin + 1));
   __syncwarp();
-  w.drain(bar(L::kFin + 1), 0, code | (L::kFin + 1));
+  w.w->drain(bar(L::kFin + 1), 0, code | (L::kFin + 1));
 }
 
 // ------------------------------------------------------------ softmax
+// out = sum_s w_s O_s / sum_s w_s over the S partial results of `rows` rows from grow0, w_s =
+// 2^(lse2_s - max), four columns of a row per thread, in the order of the splits.
+template <int D>
+__device__ __noinline__ void merge_rows8(const Dec8Params& p, size_t grow0, int rows) {
+  constexpr int Q = D / 4;
+  const int S = p.num_splits;
+#pragma unroll 1
+  for (int t = threadIdx.x; t < rows * Q; t += kWg) {
+    const size_t row = grow0 + t / Q;
+    const int c = t % Q * 4;
+    const float* pl = p.part_lse + row * S;
+    const float* po = p.part_o + row * S * D + c;
+    float top = -INFINITY;
+#pragma unroll 4
+    for (int k = 0; k < S; ++k) top = fmaxf(top, __ldcg(pl + k));
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float wsum = 0.f;
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+    for (int k = 0; k < S; ++k) {   // a split that saw nothing wrote zeros and lse -inf
+      const float wgt = dec_exp2(__ldcg(pl + k) - base);
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(po + static_cast<size_t>(k) * D));
+      wsum += wgt;
+      sum.x = fmaf(wgt, o.x, sum.x);
+      sum.y = fmaf(wgt, o.y, sum.y);
+      sum.z = fmaf(wgt, o.z, sum.z);
+      sum.w = fmaf(wgt, o.w, sum.w);
+    }
+    const float inv = wsum != 0.f ? 1.f / wsum : 0.f;
+    uint2 h;
+    h.x = attn_sm100_dec::dec_pack_bf16x2(sum.x * inv, sum.y * inv);
+    h.y = attn_sm100_dec::dec_pack_bf16x2(sum.z * inv, sum.w * inv);
+    *reinterpret_cast<uint2*>(p.out + row * D + c) = h;
+    if (c == 0) p.lse[row] = wsum != 0.f ? (top + __log2f(wsum)) * kLn2 : -INFINITY;
+  }
+}
+
 template <int D, int NR>
 __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbase, uint8_t* smem, uint32_t tmem,
-                                              const DecWaiter& w) {
+                                              const Waiter8& w) {
   using L = Smem8<D, NR>;
   auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
   constexpr int CH = NR / 16;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int wg = tid >> 7, key = tid & 127, warp = key >> 5;  // key: this thread's key of a tile
+  const int key = threadIdx.x, lane = key & 31, warp = key >> 5;  // key: this thread's key of a tile
   const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-  float* fr_all = reinterpret_cast<float*>(smem + L::kFrOff);
-  float* negm = reinterpret_cast<float*>(smem + L::kNegMOff) + wg * NR;
-  int* row_hi = reinterpret_cast<int*>(smem + L::kHiOff) + wg * NR;
-  int* row_lo = reinterpret_cast<int*>(smem + L::kLoOff) + wg * NR;
-  float* wmax = reinterpret_cast<float*>(smem + L::kWmaxOff) + wg * 4 * NR;
-  float* lsum_all = reinterpret_cast<float*>(smem + L::kLsumOff);
+  const float* fr_all = reinterpret_cast<const float*>(smem + L::kFrOff);
+  float* negm_all = reinterpret_cast<float*>(smem + L::kNegMOff);
+  int* row_hi = reinterpret_cast<int*>(smem + L::kHiOff);
+  int* row_lo = reinterpret_cast<int*>(smem + L::kLoOff);
+  float* wmax = reinterpret_cast<float*>(smem + L::kWmaxOff);
   float* coef = reinterpret_cast<float*>(smem + L::kCoefOff);
-  const float* negm_all = reinterpret_cast<float*>(smem + L::kNegMOff);
-  const int wg_bar = 1 + wg;         // barrier of the warpgroup; 3: of both
+  constexpr int kBar = 1;
   const int code = kDRoleSoftmax << 8;
   const int S = p.num_splits;
   uint32_t g = 0, items = 0, k_item = 0;
-  bool ok = true;
+  bool failed = false;
 
-  while (ok) {
-    const int idx = take_item8<L>(sbase, smem, w, k_item, code);
-    // An item that could not be taken is the end, or an abort that every warp will see: the
-    // barriers below are reached by all warps or by none, as a wait that gives up is
-    // agreed on at each barrier and an item is taken by all or missed for good.
-    if (bar_or(3, 2 * kWg, idx == -1)) break;
-    if (idx < 0) break;
-    const Item8 it = item8(p, idx);
+  // What the threads of an item ask for ahead: the scales of this thread's key, loaded a tile
+  // ahead, and their page-table entry two tiles ahead.
+  auto pos_of = [&](const Item8& it, int j) -> int {
+    if (it.t0 + j > it.t1) return -1;
+    const int pos = it.tile(it.t0 + j) * kKeys + key;
+    return it.seen(pos) ? pos : -1;
+  };
+  auto entry_of = [&](const Item8& it, int pos) -> int {
+    return pos < 0 ? 0 : __ldg(p.block_table + static_cast<size_t>(it.b) * p.max_pages + (pos >> p.page_shift));
+  };
+  auto scales_of = [&](const Item8& it, int pos, int entry, float& ks, float& vs) {
+    ks = 0.f;
+    vs = 1.f;
+    if (pos < 0) return;
+    const int page = (entry < 0 || entry >= p.num_pages) ? 0 : entry;
+    const size_t at = (static_cast<size_t>(page) * p.Hkv + it.hkv) * p.blocks_per_page +
+                      ((pos & (p.page_size - 1)) >> p.block_shift);
+    ks = __ldg(p.k_scale + at);
+    vs = __ldg(p.v_scale + at);
+  };
+
+  Item8 it = take_item8<L>(sbase, smem, w, k_item, code);
+  float ks, vs;
+  int pos_next, entry_next;
+  {
+    const int pos = pos_of(it, 0), entry = entry_of(it, pos);
+    pos_next = pos_of(it, 1);
+    entry_next = entry_of(it, pos_next);
+    scales_of(it, pos, entry, ks, vs);
+  }
+#pragma unroll 1
+  while (true) {
+    // -1: this warp's wait gave up.  Every warp gets here with the same item otherwise.
+    if (bar_or(kBar, kWg, failed || it.idx == -1) || it.idx < 0) break;
     const size_t grow0 = (static_cast<size_t>(it.b) * p.Hq + static_cast<size_t>(it.hkv) * p.group) * p.Nq + it.row0;
-    // This item's partial result is written: the CTA whose item is the last of its rows to get
-    // here merges all S of them (out = sum_s w_s O_s / sum_s w_s, w_s = 2^(lse2_s - max)), four
-    // columns of a row per thread.
-    auto merge_if_last = [&]() {
-      if (!p.done) return;
-      __threadfence();
-      bool last = false;
-      bar_or(3, 2 * kWg, false);
-      if (tid == 0) {
-        unsigned int* count = p.done + idx / S;
-        last = atomicAdd(count, 1u) == static_cast<unsigned>(S - 1);
-        if (last) atomicExch(count, 0u);
-        __threadfence();
-      }
-      if (!bar_or(3, 2 * kWg, last)) return;
-      constexpr int Q = D / 4;
-      for (int t = tid; t < it.rows * Q; t += 2 * kWg) {
-        const size_t row = grow0 + t / Q;
-        const int c = t % Q * 4;
-        const float* pl = p.part_lse + row * S;
-        const float* po = p.part_o + row * S * D + c;
-        float top = -INFINITY;
-        for (int k = 0; k < S; ++k) top = fmaxf(top, __ldcg(pl + k));
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        float wsum = 0.f;
-        const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-        for (int k = 0; k < S; ++k) {
-          const float l2 = __ldcg(pl + k), wgt = dec_exp2(l2 - base);
-          if (l2 != -INFINITY) {   // a split that saw nothing wrote no O
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(po + static_cast<size_t>(k) * D));
-            wsum += wgt;
-            sum.x = fmaf(wgt, o.x, sum.x);
-            sum.y = fmaf(wgt, o.y, sum.y);
-            sum.z = fmaf(wgt, o.z, sum.z);
-            sum.w = fmaf(wgt, o.w, sum.w);
-          }
-        }
-        const float inv = wsum != 0.f ? 1.f / wsum : 0.f;
-        uint2 h;
-        h.x = attn_sm100_dec::dec_pack_bf16x2(sum.x * inv, sum.y * inv);
-        h.y = attn_sm100_dec::dec_pack_bf16x2(sum.z * inv, sum.w * inv);
-        *reinterpret_cast<uint2*>(p.out + row * D + c) = h;
-        if (c == 0) p.lse[row] = wsum != 0.f ? (top + __log2f(wsum)) * kLn2 : -INFINITY;
-      }
-    };
-    if (it.t1 < it.t0) {
-      if (it.bad && tid == 0) atomicCAS(p.err, 0, kDErrSeqLen | (it.b & 0xFFFFF));
-      for (int e = tid; e < it.rows; e += 2 * kWg) {
-        if (S > 1) {
-          p.part_lse[(grow0 + e) * S + it.s] = -INFINITY;
-        } else {
-          p.lse[grow0 + e] = -INFINITY;
-          for (int c = 0; c < D; ++c) p.out[(grow0 + e) * D + c] = __float2bfloat16_rn(0.f);
-        }
-      }
-      if (S > 1) merge_if_last();
-      continue;
-    }
     const int n = it.t1 - it.t0 + 1;
     const uint32_t qbuf = items & 1;
     const float* fr = fr_all + qbuf * NR;
-    bool failed = !w.wait_warp(bar(L::kQFull + qbuf), (items >> 1) & 1, code | (L::kQFull + qbuf));
-    for (int r = key; r < NR; r += kWg) {
-      const int qpos = it.L - p.Nq + (it.row0 + r) % p.Nq;
-      const bool live = r < it.rows;
-      negm[r] = live ? kTop - kNoMax : -1e30f;   // rows that are not there keep weights of zero
-      row_hi[r] = live ? (p.mask_kind == kDMaskFull ? it.L - 1 : qpos) : -1;
-      row_lo[r] = p.mask_kind == kDMaskWindow ? qpos - p.window + 1 : 0;
+    if (n > 0) failed = !w.wait_warp(bar(L::kQFull + qbuf), (items >> 1) & 1, code | (L::kQFull + qbuf));
+    else if (it.bad && key == 0) atomicCAS(p.err, 0, kDErrSeqLen | (it.b & 0xFFFFF));
+    uint32_t mbuf = 0;  // which negm is current
+    if (key < NR) {
+      const int qpos = it.L - p.Nq + (it.row0 + key) % p.Nq;
+      const bool live = key < it.rows;
+      negm_all[key] = live ? kTop - kNoMax : -1e30f;   // rows that are not there keep weights of zero
+      row_hi[key] = live ? (p.mask_kind == kDMaskFull ? it.L - 1 : qpos) : -1;
+      row_lo[key] = p.mask_kind == kDMaskWindow ? qpos - p.window + 1 : 0;
     }
-    if (bar_or(wg_bar, kWg, failed)) ok = false;  // both warpgroups leave at the item's end
+    bool ok = !bar_or(kBar, kWg, failed);
     // Positions that every row sees: [all_lo, all_hi], and the sinks up to all_hi.
     const int all_hi = p.mask_kind == kDMaskFull ? it.L - 1 : it.L - p.Nq;
     const int all_lo = p.mask_kind == kDMaskWindow ? it.L - p.window : 0;
@@ -656,159 +700,120 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
     float l[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) l[r] = 0.f;
-    // Scales of this thread's key, loaded a tile ahead, their page-table entry two ahead.
-    const int* trow = p.block_table + static_cast<size_t>(it.b) * p.max_pages;
-    auto pos_of = [&](int j) -> int {
-      if (j >= n) return -1;
-      const int pos = it.tile(it.t0 + j) * kKeys + key;
-      return it.seen(pos) ? pos : -1;
-    };
-    auto entry_of = [&](int pos) -> int { return pos < 0 ? 0 : __ldg(trow + (pos >> p.page_shift)); };
-    auto scales_of = [&](int pos, int entry, float& ks, float& vs) {
-      ks = 0.f;
-      vs = 1.f;
-      if (pos < 0) return;
-      const int page = (entry < 0 || entry >= p.num_pages) ? 0 : entry;
-      const size_t at = (static_cast<size_t>(page) * p.Hkv + it.hkv) * p.blocks_per_page +
-                        ((pos & (p.page_size - 1)) >> p.block_shift);
-      ks = __ldg(p.k_scale + at);
-      vs = __ldg(p.v_scale + at);
-    };
-    const int j0 = static_cast<int>((wg - g) & 1u);
-    float ks, vs;
-    int pos_next = pos_of(j0 + 2), entry_next = entry_of(pos_next);
-    {
-      const int pos = pos_of(j0);
-      scales_of(pos, entry_of(pos), ks, vs);
-    }
-    bool any_pv = false;
-    for (int j = j0; ok && j < n; j += 2) {
-      const uint32_t gi = g + j;
-      float ks_next, vs_next;
-      scales_of(pos_next, entry_next, ks_next, vs_next);
-      const int pos_2 = pos_of(j + 4), entry_2 = entry_of(pos_2);
-      const int base = it.tile(it.t0 + j) * kKeys, pos = base + key;
-      const bool whole = base + kKeys - 1 <= all_hi && (base >= all_lo || base + kKeys <= it.sinks);
+#pragma unroll 1
+    for (int j = 0; ok && j < n; ++j) {
+      const uint32_t gi = g + j, sb = gi % L::kSBufs;
+      // This tile's scales are used before the next tile's are asked for: the loads share a
+      // scoreboard, and a use behind the newer loads waited for those too (850 cycles a tile).
       const float vsc = fminf(fmaxf(vs, kScaleMin), kScaleMax);
-      const float lv = __log2f(vsc), ivs = __frcp_rn(vsc);
-      if (!failed) failed = !w.wait_warp(bar(L::kSFull + (gi & 3)), (gi >> 2) & 1, code | (L::kSFull + (gi & 3)));
-      // The previous P V of this warpgroup is done: its P may be overwritten and O rescaled.
-      if (!failed && (gi >> 1) > 0)
-        failed = !w.wait_warp(bar(L::kPVDone + wg), ((gi >> 1) - 1) & 1, code | (L::kPVDone + wg));
+      const float lv = __log2f(vsc), ivs = __frcp_rn(vsc), ksl = ks * p.scale_log2;
+      asm volatile("" ::"f"(lv), "f"(ivs), "f"(ksl) : "memory");
+      scales_of(it, pos_next, entry_next, ks, vs);
+      pos_next = pos_of(it, j + 2);
+      entry_next = entry_of(it, pos_next);
+      const int base = it.tile(it.t0 + j) * kKeys, pos = base + key;
+      failed |= !w.wait_warp(bar(L::kSFull + sb), (gi / L::kSBufs) & 1, code | (L::kSFull + sb));
       tc_fence_after_sync();
-      const uint32_t s_addr = lane_addr + L::kSCol + (gi & 3) * L::kSCols;
-      // e[i] = y - m + kTop of rows 16 ch + i (the exponent of the weight), -inf where masked.
-      auto exponents = [&](int ch, float add, bool with_m, float (&e)[16]) {
-        uint32_t sr[16];
-        if constexpr (L::kWide) {
-          uint32_t s2[16];
-          tmem_load_2x16cols(s_addr + ch * 16, s_addr + NR + ch * 16, sr, s2);
+      // y_r = x_r + log2 c of this key and every row, -inf where the row does not see the key.
+      float y[NR];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) sr[i] = __float_as_uint(__uint_as_float(sr[i]) + __uint_as_float(s2[i]));
-        } else {
-          tmem_load_16cols(s_addr + ch * 16, sr);
-        }
+      for (int ch = 0; ch < CH; ++ch) {
+        const uint32_t s_addr = lane_addr + L::kSCol + sb * L::kSCols + ch * 16;
+        uint32_t s1[16], s2[16];
+        tmem_load_2x16cols(s_addr, s_addr + NR, s1, s2);
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 f4 = *reinterpret_cast<const float4*>(fr + ch * 16 + i);
-          const float4 m4 = *reinterpret_cast<const float4*>(negm + ch * 16 + i);
-          const float ff[4] = {f4.x, f4.y, f4.z, f4.w}, mm[4] = {m4.x, m4.y, m4.z, m4.w};
+          const float ff[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            e[i + k] = fmaf(__uint_as_float(sr[i + k]) * ks, ff[k], with_m ? add + mm[k] : add);
-        }
-        if (!whole) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int r = ch * 16 + i;
-            if (pos > row_hi[r] || (pos < row_lo[r] && pos >= it.sinks)) e[i] = -INFINITY;
-          }
-        }
-      };
-      // Up to 32 rows' exponents stay in registers; of 64 rows the first 16's do, and the
-      // others' are formed again below.
-      constexpr int kKeep = CH <= 2 ? CH : 1;
-      float e[kKeep][16];
-      float top = -INFINITY;
-      if (!failed) {
-#pragma unroll
-        for (int ch = CH - 1; ch >= 0; --ch) {
-          exponents(ch, lv, true, e[ch % kKeep]);
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) top = max3f(top, e[ch % kKeep][i], e[ch % kKeep][i + 1]);
+            y[ch * 16 + i + k] = fmaf((__uint_as_float(s1[i + k]) + __uint_as_float(s2[i + k])) * ksl, ff[k], lv);
         }
       }
-      if (bar_or(wg_bar, kWg, failed || top > kTop + kGrow)) {
-        // Some row's maximum grew (or some warp gives up): every warp's row maxima.
-        if (!failed) {
+      if (!(base + kKeys - 1 <= all_hi && (base >= all_lo || base + kKeys <= it.sinks))) {
+        uint32_t hidden = 0;
 #pragma unroll 1
-          for (int ch = 0; ch < CH; ++ch) {
-            float y[16];
-            exponents(ch, lv, false, y);
-            int mine = 0;
+        for (int r = 0; r < NR; ++r)
+          hidden |= ((pos > row_hi[r]) | ((pos < row_lo[r]) & (pos >= it.sinks)) ? 1u : 0u) << r;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int m = __reduce_max_sync(0xffffffffu, ordered(y[i]));
-              if (lane == i) mine = m;
-            }
-            if (lane < 16) wmax[warp * NR + ch * 16 + lane] = unordered(mine);
-          }
+        for (int r = 0; r < NR; ++r)
+          if (hidden & (1u << r)) y[r] = -INFINITY;
+      }
+      // e = y - m + kTop, the exponents of the weights, unless some row's maximum has grown.
+      const float* negm = negm_all + mbuf * NR;
+      bool grown = j == 0;  // an item's first tile sets the maxima
+      if (j > 0) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < NR; r += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(negm + r);
+          top = max3f(top, y[r] + m4.x, y[r + 1] + m4.y);
+          top = max3f(top, y[r + 2] + m4.z, y[r + 3] + m4.w);
         }
-        if (bar_or(wg_bar, kWg, failed)) {
+        grown = bar_or(kBar, kWg, failed || top > kTop + kGrow);
+      }
+      // The last product has read P, and O may be changed.
+      if (!failed && gi > 0) failed = !w.wait_warp(bar(L::kPVDone), (gi - 1) & 1, code | L::kPVDone);
+      if (grown) {
+        // Every warp's row maxima, then m and factor of every row: a row's m moves to its
+        // maximum when that is more than kGrow above it.
+        tc_fence_after_sync();
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) {
+          int mine = 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int m = __reduce_max_sync(0xffffffffu, ordered(y[ch * 16 + i]));
+            if (lane == i) mine = m;
+          }
+          if (lane < 16) wmax[warp * NR + ch * 16 + lane] = unordered(mine);
+        }
+        if (bar_or(kBar, kWg, failed)) {
           ok = false;
           break;
         }
-        float mine_new = 0.f;
-        // negm' and factor of every row; a row's m moves to its maximum when that is kGrow above it.
-#pragma unroll
-        for (int ch = 0; ch < CH; ++ch) {
-          float f[16];
-          bool any = false;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int r = ch * 16 + i;
-            const float mx = fmaxf(fmaxf(wmax[r], wmax[NR + r]), fmaxf(wmax[2 * NR + r], wmax[3 * NR + r]));
-            const float old = negm[r];
-            const bool move = mx + old > kTop + kGrow && mx < INFINITY;
-            const float now = move ? kTop - mx : old;
-            f[i] = move ? dec_exp2(now - old) : 1.f;
-            any |= move;
-            if (key == r) mine_new = now;
-            l[r] *= f[i];
-          }
-          if (any && any_pv) {
-#pragma unroll
-            for (int term = 0; term < (L::kWide ? 3 : 1); ++term) {
-              uint32_t o[16];
-              const uint32_t at = lane_addr + L::kOCol + wg * L::kOCols + term * NR + ch * 16;
-              tmem_load_16cols(at, o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i]);
-              tmem_store_16cols(at, o);
-            }
-          }
+        // Thread r < NR moves row r; every thread then applies the factors.
+        if (key < NR) {
+          const float mx = fmaxf(fmaxf(wmax[key], wmax[NR + key]), fmaxf(wmax[2 * NR + key], wmax[3 * NR + key]));
+          const float old = negm[key];
+          const bool move = mx + old > kTop + kGrow && mx < INFINITY;
+          const float now = move ? kTop - mx : old;
+          negm_all[(mbuf ^ 1) * NR + key] = now;
+          coef[key] = move ? dec_exp2(now - old) : 1.f;
         }
-        tmem_store_wait();
-        bar_or(wg_bar, kWg, false);   // every thread has read the old maxima
-        if (key < NR) negm[key] = mine_new;
-        bar_or(wg_bar, kWg, false);
+        bar_or(kBar, kWg, false);
+        mbuf ^= 1;
+        negm = negm_all + mbuf * NR;
+        if (j > 0) {
 #pragma unroll
-        for (int ch = kKeep - 1; ch >= 0; --ch) exponents(ch, lv, true, e[ch]);
+          for (int r = 0; r < NR; ++r) l[r] *= coef[r];
+#pragma unroll 1
+          for (int c = 0; c < 3 * NR; c += 16) {
+            uint32_t o[16];
+            const uint32_t at = lane_addr + L::kOCol + c;
+            const float* f = coef + c % NR;
+            tmem_load_16cols(at, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f[i]);
+            tmem_store_16cols(at, o);
+          }
+          tmem_store_wait();
+        }
       }
       // Weights, their sum, and their three E5M2 terms: a weight in fp16 (11 significant
       // bits), whose upper byte is an E5M2 number; what that leaves, likewise; the last
       // remainder rounded to nearest.
-      const uint32_t p_addr = sbase + L::kPOff + wg * L::kPBuf + key * 16;
+      const uint32_t p_addr = sbase + L::kPOff + key * 16;
 #pragma unroll
       for (int ch = 0; ch < CH; ++ch) {
-        if (ch >= kKeep) exponents(ch, lv, true, e[ch % kKeep]);
-        const float(&e0)[16] = e[ch % kKeep];
         uint32_t t1[8], t2[8], t3[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float a = dec_exp2(e0[2 * i]), b = dec_exp2(e0[2 * i + 1]);
-          l[ch * 16 + 2 * i] = fmaf(a, ivs, l[ch * 16 + 2 * i]);
-          l[ch * 16 + 2 * i + 1] = fmaf(b, ivs, l[ch * 16 + 2 * i + 1]);
+          const int r = ch * 16 + 2 * i;
+          const float2 m2 = *reinterpret_cast<const float2*>(negm + r);
+          const float a = dec_exp2(y[r] + m2.x), b = dec_exp2(y[r + 1] + m2.y);
+          l[r] = fmaf(a, ivs, l[r]);
+          l[r + 1] = fmaf(b, ivs, l[r + 1]);
           const uint32_t h = pack_f16x2(a, b);
           t1[i] = h & 0xff00ff00u;
           const uint32_t r1 = half2_sub(h, t1[i]);
@@ -826,10 +831,10 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       }
       if (base + kKeys > it.L || (base < it.lo_pos && base + kKeys > it.sinks)) {
         // Rows of V that the step does not see were not loaded, or hold anything: zero them.
-        const uint32_t vi = 2 * gi + 1, slot = vi % L::kStages;
-        failed = !w.wait_warp(bar(L::kKVFull + slot), (vi / L::kStages) & 1, code | (L::kKVFull + slot));
+        const uint32_t slot = gi % L::kVSlots;
+        failed |= !w.wait_warp(bar(L::kVFull + slot), (gi / L::kVSlots) & 1, code | (L::kVFull + slot));
         if (!failed && !it.seen(pos)) {
-          const uint32_t at = sbase + L::kRingOff + slot * L::kTileBytes + key * D;
+          const uint32_t at = sbase + L::kVOff + slot * L::kTileBytes + key * D;
 #pragma unroll
           for (int c = 0; c < D; c += 16) st_shared_v4(at + c, 0u, 0u, 0u, 0u);
         }
@@ -838,113 +843,97 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar(L::kPFull + wg));
-        mbar_arrive(bar(L::kSFree + (gi & 3)));
+        mbar_arrive(bar(L::kPFull));
+        mbar_arrive(bar(L::kSFree + sb));
       }
-      any_pv = true;
-      ks = ks_next;
-      vs = vs_next;
-      pos_next = pos_2;
-      entry_next = entry_2;
     }
-    // ---- epilogue: this warpgroup's O is complete; sums over its keys.
+    // ---- the item's end: the last product, the sums over the keys, the rows.  In between,
+    // the next item's page entries and scales are asked for.
     failed |= !ok;
-    if (!failed && any_pv) {
-      const uint32_t last = (g + n - 1 - ((g + n - 1 - wg) & 1u)) >> 1;
-      failed = !w.wait_warp(bar(L::kPVDone + wg), last & 1, code | (L::kPVDone + wg));
-    }
-    if (!failed) {
-      // Sixteen sums over 32 lanes: each step halves the rows a lane carries.
+    const Item8 nx = take_item8<L>(sbase, smem, w, k_item, code);
+    const int npos = pos_of(nx, 0), nentry = entry_of(nx, npos);
+    pos_next = pos_of(nx, 1);
+    entry_next = entry_of(nx, pos_next);
+    // Sixteen sums over 32 lanes: each step halves the rows a lane carries.
 #pragma unroll
-      for (int ch = 0; ch < CH; ++ch) {
-        float v[16];
+    for (int ch = 0; ch < CH; ++ch) {
+      float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = l[ch * 16 + i];
+      for (int i = 0; i < 16; ++i) v[i] = l[ch * 16 + i];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-          const bool up = lane & o;
+      for (int o = 8; o > 0; o >>= 1) {
+        const bool up = lane & o;
 #pragma unroll
-          for (int i = 0; i < o; ++i) {
-            const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-          }
+        for (int i = 0; i < o; ++i) {
+          const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
-        if (lane < 16) lsum_all[(wg * 4 + warp) * NR + ch * 16 + lane] = v[0];
       }
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+      if (lane < 16) wmax[warp * NR + ch * 16 + lane] = v[0];
     }
-    if (lane == 0) mbar_arrive(bar(L::kQEmpty + qbuf));  // this warp has read the row factors
-    if (bar_or(3, 2 * kWg, failed)) {
-      ok = false;
-      break;
+    if (n > 0) {
+      if (!failed) failed = !w.wait_warp(bar(L::kPVDone), (g + n - 1) & 1, code | L::kPVDone);
+      if (lane == 0) mbar_arrive(bar(L::kQEmpty + qbuf));  // this warp has read the row factors
     }
+    if (bar_or(kBar, kWg, failed)) break;
     tc_fence_after_sync();
-    for (int r = tid; r < NR; r += 2 * kWg) {
-      const float n0 = negm_all[r], n1 = negm_all[NR + r];
-      const float top = fminf(n0, n1);   // kTop - the larger maximum
-      const float f0 = dec_exp2(top - n0), f1 = dec_exp2(top - n1);
-      float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        s0 += lsum_all[k * NR + r];
-        s1 += lsum_all[(4 + k) * NR + r];
-      }
-      const float sum = f0 * s0 + f1 * s1;
-      const float inv = sum != 0.f ? 1.f / sum : 0.f;   // (a NaN sum stays NaN)
-      coef[r] = f0 * inv;
-      coef[NR + r] = f1 * inv;
-      if (r < it.rows) {
-        const float l2 = sum != 0.f ? __log2f(sum) - top : -INFINITY;
-        if (S > 1) p.part_lse[(grow0 + r) * S + it.s] = l2;
-        else p.lse[grow0 + r] = l2 * kLn2;
-      }
+    if (key < it.rows) {
+      const float top = negm_all[mbuf * NR + key];   // kTop - m
+      const float sum = (wmax[key] + wmax[NR + key]) + (wmax[2 * NR + key] + wmax[3 * NR + key]);
+      coef[key] = sum != 0.f ? 1.f / sum : 0.f;      // (a NaN sum stays NaN; nothing seen: zero)
+      const float l2 = sum != 0.f ? __log2f(sum) - top : -INFINITY;
+      if (S > 1) p.part_lse[(grow0 + key) * S + it.s] = l2;
+      else p.lse[grow0 + key] = l2 * kLn2;
     }
-    bar_or(3, 2 * kWg, false);
-    // Rows are dealt to the two warpgroups in halves; thread = column of d.
-    const bool has0 = n > 1 || (g & 1) == 0, has1 = n > 1 || (g & 1) == 1;
-    constexpr int kHalf = NR / 2 < 16 ? NR / 2 : 16;
+    scales_of(nx, npos, nentry, ks, vs);
+    bar_or(kBar, kWg, false);
+    // Thread = column of d.  An item without tiles has no O: its rows are zero (one split), or
+    // carry no weight in the merge.
 #pragma unroll 1
-    for (int c0 = wg * (NR / 2); c0 < (wg + 1) * (NR / 2); c0 += kHalf) {
-      if (c0 >= it.rows) break;
-      uint32_t a[16], b[16];
-      // 16 columns even where 8 are used: the columns behind belong to the other half.
-      const int col = NR == 16 ? 0 : c0;
-      auto load_o = [&](int g2, uint32_t (&o)[16]) {
-        const uint32_t at = lane_addr + L::kOCol + g2 * L::kOCols + col;
-        tmem_load_16cols(at, o);
-        if constexpr (L::kWide) {
-          uint32_t o2[16], o3[16];
-          tmem_load_2x16cols(at + NR, at + 2 * NR, o2, o3);
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            o[i] = __float_as_uint(__uint_as_float(o[i]) + (__uint_as_float(o2[i]) + __uint_as_float(o3[i])));
-        }
-      };
-      if (has0) load_o(0, a);
-      if (has1) load_o(1, b);
+    for (int r0 = 0; r0 < it.rows; r0 += 16) {
+      uint32_t o[16], o2[16], o3[16];
+      const uint32_t at = lane_addr + L::kOCol + r0;
+      tmem_load_16cols(at, o);
+      tmem_load_2x16cols(at + NR, at + 2 * NR, o2, o3);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int r = col + i;
-        if (r >= c0 && r < c0 + kHalf && r < it.rows && key < D) {
-          float v = 0.f;
-          if (has0) v = __uint_as_float(a[i]) * coef[r];
-          if (has1) v = fmaf(__uint_as_float(b[i]), coef[NR + r], v);
+        const int r = r0 + i;
+        if (r < it.rows && key < D) {
+          float v = (__uint_as_float(o[i]) + (__uint_as_float(o2[i]) + __uint_as_float(o3[i]))) * coef[r];
+          if (n <= 0) v = 0.f;
           if (S > 1) p.part_o[((grow0 + r) * S + it.s) * D + key] = v;
           else p.out[(grow0 + r) * D + key] = __float2bfloat16_rn(v);
         }
       }
     }
-    tc_fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(L::kOFree));
-    if (S > 1) merge_if_last();
-    g += n;
-    ++items;
+    if (n > 0) {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kOFree));
+      g += n;
+      ++items;
+    }
+    if (p.done) {
+      // This item's partial result is written: the CTA whose item is the last of its unit to
+      // get here merges them all.
+      __threadfence();
+      bool last = false;
+      bar_or(kBar, kWg, false);
+      if (key == 0) {
+        unsigned int* count = p.done + it.unit;
+        last = atomicAdd(count, 1u) == static_cast<unsigned>(S - 1);
+        if (last) atomicExch(count, 0u);
+        __threadfence();
+      }
+      if (bar_or(kBar, kWg, last)) merge_rows8<D>(p, grow0, it.rows);
+    }
+    it = nx;
   }
 }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kThreads, 1) attn_decode8_kernel(const __grid_constant__ Dec8Params p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode8_kernel(const __grid_constant__ Dec8Params p) {
   using L = Smem8<D, NR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -957,24 +946,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode8_kernel(const __grid_
     auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::kQFull + i), 1);
-      mbar_init(bar(L::kQEmpty + i), 9);  // the last S product and the eight softmax warps
-      mbar_init(bar(L::kPFull + i), 4);
-      mbar_init(bar(L::kPVDone + i), 1);
+      mbar_init(bar(L::kQEmpty + i), 5);  // the last S product and the softmax warps
+      mbar_init(bar(L::kFin + i), 1);
     }
-    for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(bar(L::kKVFull + s), 1);
-      mbar_init(bar(L::kKVEmpty + s), 1);
-    }
-    for (int i = 0; i < 4; ++i) {
+    mbar_init(bar(L::kPFull), 4);
+    mbar_init(bar(L::kPVDone), 1);
+    mbar_init(bar(L::kOFree), 4);
+    for (int s = 0; s < 2 * L::kKSlots; ++s) mbar_init(bar(L::kKFull + s), 1);  // full and empty
+    for (int s = 0; s < 2 * L::kVSlots; ++s) mbar_init(bar(L::kVFull + s), 1);
+    for (int i = 0; i < L::kSBufs; ++i) {
       mbar_init(bar(L::kSFull + i), 1);
       mbar_init(bar(L::kSFree + i), 4);
     }
-    mbar_init(bar(L::kOFree), 8);
-    mbar_init(bar(L::kFin), 1);
-    mbar_init(bar(L::kFin + 1), 1);
     for (int i = 0; i < kItemSlots; ++i) {
       mbar_init(bar(L::kItemFull + i), 1);
-      mbar_init(bar(L::kItemEmpty + i), 11);  // every warp but the K loader
+      mbar_init(bar(L::kItemEmpty + i), 7);  // every warp but the K loader
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -987,16 +973,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode8_kernel(const __grid_
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const DecWaiter w{p.timeout_ns, abort_flag, p.err};
+  const DecWaiter bounded{p.timeout_ns, abort_flag, p.err};
+  const Waiter8 w{&bounded};
 
-  if (warp < 8) {
+  if (warp < 4) {
     softmax_role8<D, NR>(p, sbase, smem, tmem, w);
-  } else if (warp == kKWarp) {
-    const uint32_t gt = loader8<D, NR, false>(p, sbase, smem, w);
-    if ((threadIdx.x & 31) == 0) loaded[0] = gt;
-  } else if (warp == kVWarp) {
-    const uint32_t gt = loader8<D, NR, true>(p, sbase, smem, w);
-    if ((threadIdx.x & 31) == 0) loaded[1] = gt;
+  } else if (warp == kKWarp || warp == kVWarp) {
+    const uint32_t gt = loader8<D, NR>(p, sbase, smem, w, warp == kVWarp);
+    if ((threadIdx.x & 31) == 0) loaded[warp - kKWarp] = gt;
   } else if (warp == kPvWarp) {
     pv_role8<D, NR>(p, sbase, smem, tmem, w);
   } else {
@@ -1004,7 +988,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode8_kernel(const __grid_
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (threadIdx.x == kKWarp * 32) drain_ring8<L>(sbase, w, loaded[0], loaded[1]);
+  if (threadIdx.x == kKWarp * 32) {
+    drain_ring8(sbase + L::kBarOff + 8u * L::kKFull, L::kKSlots, bounded, loaded[0]);
+    drain_ring8(sbase + L::kBarOff + 8u * L::kVFull, L::kVSlots, bounded, loaded[1]);
+  }
   if (warp == kPvWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, L::kTmemCols);

@@ -344,6 +344,18 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a0, float a1, float a2, fl
   return r;
 }
 
+// The four values of a word of E4M3 codes (bits 0..7 first).
+__device__ __forceinline__ void e4m3x4_values(uint32_t w, float& a0, float& a1, float& a2, float& a3) {
+  asm("{\n\t.reg .b16 lo, hi, x, y;\n\t.reg .b32 p, q;\n\t"
+      "mov.b32 {lo, hi}, %4;\n\t"
+      "cvt.rn.f16x2.e4m3x2 p, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 q, hi;\n\t"
+      "mov.b32 {x, y}, p;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t"
+      "mov.b32 {x, y}, q;\n\tcvt.f32.f16 %2, x;\n\tcvt.f32.f16 %3, y;\n\t}"
+      : "=f"(a0), "=f"(a1), "=f"(a2), "=f"(a3)
+      : "r"(w));
+}
+
 // 32-byte global store (sm_100); ptr must be 32-byte aligned.
 __device__ __forceinline__ void st_global_v8(void* ptr, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
                                              uint32_t f, uint32_t g, uint32_t h) {
