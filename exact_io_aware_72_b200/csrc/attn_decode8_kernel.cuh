@@ -28,7 +28,7 @@
 //   and a weight is lost only below 2^-26 of the largest.
 // * Sums l and all statistics are fp32; out is rounded once to bf16.
 //
-// Work items, splits and the item counter are the bf16 decoding kernel's.  Two CTAs share an
+// Work items and splits are the bf16 decoding kernel's.  Two CTAs share an
 // SM, each with its own items, ring and softmax warpgroup: at an item's ends (its first page
 // entries and scales, the last product, the merge) one CTA's chain of latencies, some 5 us,
 // runs under the other's tiles.  (One CTA whose two warpgroups took the tiles of an item in
@@ -325,9 +325,11 @@ __device__ __forceinline__ uint32_t loader8(const Dec8Params& p, uint32_t sbase,
   if (lane == 0) tma_prefetch_map(map);
   const int code = kDRoleLoader << 8;
   uint32_t gt = 0, k_item = 0, slot = 0, round = 0;  // tile gt goes to `slot`, filled `round` times before
-  int next = 0;
+  // A CTA's first item is its own number, the others come from the counter: fetched one ahead
+  // from the start, the CTAs that came first would hold two items each of a single wave.
+  int next = blockIdx.x;
   auto fetch = [&]() {
-    if (lane == 0) next = static_cast<int>(atomicAdd(p.sched, 1u));
+    if (lane == 0) next = static_cast<int>(gridDim.x + atomicAdd(p.sched, 1u));
   };
   // Decodes and publishes the fetched item (or the end), and fetches another.
   auto publish = [&](Item8& it) -> bool {
@@ -353,10 +355,7 @@ __device__ __forceinline__ uint32_t loader8(const Dec8Params& p, uint32_t sbase,
     return true;
   };
   Item8 it, nx;
-  if (!kv) {
-    fetch();
-    if (!publish(it)) return 0;
-  }
+  if (!kv && !publish(it)) return 0;
   while (true) {
     if (kv) {
       it = take_item8<L>(sbase, smem, w, k_item, code);
@@ -600,12 +599,12 @@ __device__ __noinline__ void merge_rows8(const Dec8Params& p, size_t grow0, int 
     const float* pl = p.part_lse + row * S;
     const float* po = p.part_o + row * S * D + c;
     float top = -INFINITY;
-#pragma unroll 4
+#pragma unroll 16
     for (int k = 0; k < S; ++k) top = fmaxf(top, __ldcg(pl + k));
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     float wsum = 0.f;
     const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
+#pragma unroll 16
     for (int k = 0; k < S; ++k) {   // a split that saw nothing wrote zeros and lse -inf
       const float wgt = dec_exp2(__ldcg(pl + k) - base);
       const float4 o = __ldcg(reinterpret_cast<const float4*>(po + static_cast<size_t>(k) * D));

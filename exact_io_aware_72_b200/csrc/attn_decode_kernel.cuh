@@ -286,8 +286,9 @@ __device__ __forceinline__ uint32_t dec_loader(const DecParams& p, uint32_t sbas
   // Work items come from the shared counter, one ahead of use so that the
   // atomic's latency overlaps the current item; each index is published to
   // the other roles before the item's loads start.
-  int next = 0;
-  if (!kV && lane == 0) next = static_cast<int>(atomicAdd(p.sched, 1u));
+  // (The first item is the CTA's own number: taken from the counter too, a single wave's
+  // items would go in pairs to the CTAs that came first.)
+  int next = blockIdx.x;
   while (ok) {
     int idx;
     if constexpr (kV) {
@@ -305,7 +306,7 @@ __device__ __forceinline__ uint32_t dec_loader(const DecParams& p, uint32_t sbas
       }
       ++k_item;
       if (idx >= p.num_items) break;
-      if (lane == 0) next = static_cast<int>(atomicAdd(p.sched, 1u));
+      if (lane == 0) next = static_cast<int>(gridDim.x + atomicAdd(p.sched, 1u));
     }
     const DecItem it = dec_item(p, idx);
     if (it.t1 < it.t0) continue;
