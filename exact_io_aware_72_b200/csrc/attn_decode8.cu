@@ -1,6 +1,6 @@
 // Host side of the 8-bit-cache decoding entry points declared in include/attn.h: argument
-// checks, TMA tensor maps over the code pools and the decoding launch (for very many units
-// with splits, the merge launch too) on the caller's stream.
+// checks, TMA tensor maps over the code pools, the decoding launch and (with more than one
+// split) the merge launch, all on the caller's stream.
 #include "attn.h"
 
 #include <cuda.h>
@@ -101,13 +101,9 @@ int log2_of(int64_t x) {
   return n;
 }
 
-// Workspace: 256 bytes of work-item counters and kMaxMerged counters of finished splits (all
-// zero between calls, at the same place whatever the sizes), then with more than one split
-// the partial log-sum-exps and the partial outputs.  A step of more than kMaxMerged
-// (sequence, KV head, row chunk) units merges its splits in a launch of its own.
-constexpr int64_t kMaxMerged = 16320;
-constexpr size_t kSchedBytes = 256 + kMaxMerged * 4;
-static_assert(kSchedBytes == 65536, "zeroed head of the workspace");
+// Workspace: 256 bytes of work-item counters (zero between calls), then with more than one
+// split the partial log-sum-exps and the partial outputs.
+constexpr size_t kSchedBytes = 256;
 size_t workspace_bytes(int64_t rows, int64_t d, int64_t splits) {
   if (splits <= 1) return kSchedBytes;
   return kSchedBytes + align_up(static_cast<size_t>(rows) * splits * 4, 256) +
@@ -250,8 +246,6 @@ extern "C" int attn_decode_kv8(const void* q, const void* k_cache, const void* v
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.sched = static_cast<unsigned int*>(workspace);
-  const bool merge_here = num_splits > 1 && B * Hkv * row_chunks <= kMaxMerged;
-  if (merge_here) p.done = p.sched + 64;
   if (num_splits > 1) {
     uint8_t* ws = static_cast<uint8_t*>(workspace) + kSchedBytes;
     p.part_lse = reinterpret_cast<float*>(ws);
@@ -286,18 +280,26 @@ extern "C" int attn_decode_kv8(const void* q, const void* k_cache, const void* v
   if (opts && opts->grid_ctas > 0) grid = std::min(grid, opts->grid_ctas);
   if ((d == 64 ? launch_rows<64>(p, grid, stream) : launch_rows<128>(p, grid, stream)) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  if (num_splits > 1 && !merge_here) {
-    attn_sm100_dec::DecMergeParams mp;
+  if (num_splits > 1) {
+    Merge8Params mp;
     mp.part_o = p.part_o;
     mp.part_lse = p.part_lse;
     mp.out = p.out;
     mp.lse = lse;
-    mp.rows = static_cast<int>(rows);
     mp.num_splits = static_cast<int>(num_splits);
-    const unsigned blocks = static_cast<unsigned>((rows + 3) / 4);
-    if (d == 64) attn_sm100_dec::attn_decode_merge_kernel<64><<<blocks, 128, 0, stream>>>(mp);
-    else attn_sm100_dec::attn_decode_merge_kernel<128><<<blocks, 128, 0, stream>>>(mp);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = static_cast<size_t>(num_splits) * sizeof(float);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = d == 64 ? cudaLaunchKernelEx(&cfg, attn_decode8_merge_kernel<64>, mp)
+                                  : cudaLaunchKernelEx(&cfg, attn_decode8_merge_kernel<128>, mp);
+    if (e != cudaSuccess) return ATTN_ERR_CUDA;
   }
   return ATTN_OK;
 }

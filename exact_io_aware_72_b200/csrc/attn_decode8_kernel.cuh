@@ -36,9 +36,10 @@
 // m is per row: a vote over the warpgroup (one hardware barrier with a reduction) finds the
 // rare tiles where some row's maximum grew by more than 2^6.
 //
-// The splits of one (sequence, KV head, row chunk) count themselves in the workspace as they
-// finish, and the CTA that finishes the last one merges their partial results, in the order
-// of the splits (a merge launch of its own took 9 us behind a 70 us step).
+// The partial results of splits are merged by a second, small kernel whose launch overlaps the
+// first one's end (programmatic dependent launch).  Merged by the CTA that finished last, they
+// kept one SM reading for 9 us behind the other 147 (37 splits of 8 rows) and cost each item a
+// fence and an atomic.
 //
 // Warps: 0-3 softmax, 4 loads K (and fetches items), 5 loads V, 6 issues the P V products, 7
 // prepares Q and issues the S products ahead.  (One issuing warp spent 1500 cycles per tile
@@ -109,7 +110,6 @@ struct Dec8Params {
   float scale_log2;
   unsigned long long timeout_ns;
   unsigned int* sched;     // [0] next work item, [1] CTAs finished; zero between launches
-  unsigned int* done;      // splits finished, per (b, KV head, row chunk); zero between launches (null: no merge here)
 };
 
 template <int D, int NR>
@@ -172,12 +172,12 @@ struct Smem8 {
 // position range's tile.
 struct __align__(16) Item8 {
   int idx;               // its number; -2: no more items
-  int b, hkv, s, unit;   // unit: number of the (b, KV head, row chunk)
+  int b, hkv, s;
   int L, lo_pos, sinks;  // cached positions; oldest position in any row's window; sinks
   int ns, first;         // tile(u) = u < ns ? u : u - ns + first
   int t0, t1;            // range of u of this split (empty when t1 < t0)
   int row0, rows;
-  int bad, pad;
+  int bad, pad[2];
   __device__ __forceinline__ int tile(int u) const { return u < ns ? u : u - ns + first; }
   __device__ __forceinline__ bool seen(int pos) const { return pos < L && (pos >= lo_pos || pos < sinks); }
 };
@@ -190,7 +190,6 @@ __device__ __forceinline__ Item8 item8(const Dec8Params& p, int idx) {
   idx /= p.row_chunks;
   it.s = idx % p.num_splits;
   idx /= p.num_splits;
-  it.unit = idx * p.row_chunks + rc;
   it.hkv = idx % p.Hkv;
   it.b = idx / p.Hkv;
   it.L = __ldg(p.seq_lens + it.b);
@@ -200,7 +199,7 @@ __device__ __forceinline__ Item8 item8(const Dec8Params& p, int idx) {
   it.lo_pos = it.ns = it.first = it.t0 = 0;
   it.sinks = 0;
   it.t1 = -1;
-  it.pad = 0;
+  it.pad[0] = it.pad[1] = 0;
   if (!it.bad && it.L > 0) {
     if (p.mask_kind == kDMaskWindow) {
       it.lo_pos = max(0, it.L - p.Nq - p.window + 1);
@@ -415,58 +414,51 @@ __device__ __forceinline__ void drain_ring8(uint32_t full, int slots, const DecW
 }
 
 // ------------------------------------------------------------ Q
-// One warp: each row of an item becomes two E4M3 terms in shared memory (K-major, in the
+// One warp: each of the rows b0 .. b1 - 1 of an item becomes two E4M3 terms in shared memory (K-major, in the
 // swizzle of a D-byte row), with its factor 1 / (the row's power of two).
 template <int D, int NR>
-__device__ __forceinline__ void prepare_q8(const Dec8Params& p, const Item8& it, uint8_t* smem, uint32_t buf) {
+__device__ __noinline__ void prepare_q8(const Dec8Params& p, const Item8& it, uint8_t* smem, uint32_t buf, int b0,
+                                        int b1) {
   using L = Smem8<D, NR>;
   constexpr int G = D / 16;          // lanes of a row, 16 elements each
   constexpr int kRows = 32 / G;      // rows of a pass
-  constexpr int kBatch = 2;          // passes whose loads are in flight together
   const int lane = threadIdx.x & 31, c = lane % G;
   const size_t row0 = (static_cast<size_t>(it.b) * p.Hq + static_cast<size_t>(it.hkv) * p.group) * p.Nq + it.row0;
   const uint4* src = reinterpret_cast<const uint4*>(p.q + row0 * D) + 2 * c;
   float* fr = reinterpret_cast<float*>(smem + L::kFrOff) + buf * NR;
   uint8_t* q1 = smem + L::kQOff + buf * L::kQBuf;
 #pragma unroll 1
-  for (int b = 0; b < NR; b += kRows * kBatch) {
-    uint4 raw[kBatch][2];
+  for (int b = b0; b < b1; b += kRows) {
+    const int r = b + lane / G;
+    const bool live = r < it.rows && r < b1;
+    const uint4 lo = live ? __ldg(src + static_cast<size_t>(r) * (D / 8)) : make_uint4(0u, 0u, 0u, 0u);
+    const uint4 hi = live ? __ldg(src + static_cast<size_t>(r) * (D / 8) + 1) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t big = 0;  // largest magnitude, bf16 bits in each half
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int r = b + k * kRows + lane / G;
-      const bool live = r < it.rows;
-      raw[k][0] = live ? __ldg(src + static_cast<size_t>(r) * (D / 8)) : make_uint4(0u, 0u, 0u, 0u);
-      raw[k][1] = live ? __ldg(src + static_cast<size_t>(r) * (D / 8) + 1) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < 8; ++i) big = max_u16x2(big, w[i] & 0x7fff7fffu);
+    big = max(big >> 16, big & 0xffffu);
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+    // Multiplier 2^(7 - exponent): the row's largest lands in [128, 256).  E4M3 has no
+    // infinities: a row that holds one (or a NaN) becomes NaN.
+    const int e = min(max(134 - static_cast<int>(big >> 7), -126), 126);
+    const float mul = big >= 0x7f80u ? __int_as_float(0x7fffffff)
+                                     : (big ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 1.f);
+    uint32_t c1[4], c2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x0 = __uint_as_float(w[2 * i] << 16) * mul, x1 = __uint_as_float(w[2 * i] & 0xffff0000u) * mul;
+      const float x2 = __uint_as_float(w[2 * i + 1] << 16) * mul;
+      const float x3 = __uint_as_float(w[2 * i + 1] & 0xffff0000u) * mul;
+      c1[i] = pack_e4m3x4(x0, x1, x2, x3);
+      float y0, y1, y2, y3;
+      e4m3x4_values(c1[i], y0, y1, y2, y3);
+      c2[i] = pack_e4m3x4(x0 - y0, x1 - y1, x2 - y2, x3 - y3);
     }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int r = b + k * kRows + lane / G;
-      const uint32_t w[8] = {raw[k][0].x, raw[k][0].y, raw[k][0].z, raw[k][0].w,
-                             raw[k][1].x, raw[k][1].y, raw[k][1].z, raw[k][1].w};
-      uint32_t big = 0;  // largest magnitude, bf16 bits in each half
-#pragma unroll
-      for (int i = 0; i < 8; ++i) big = max_u16x2(big, w[i] & 0x7fff7fffu);
-      big = max(big >> 16, big & 0xffffu);
-#pragma unroll
-      for (int o = G / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-      // Multiplier 2^(7 - exponent): the row's largest lands in [128, 256).  E4M3 has no
-      // infinities: a row that holds one (or a NaN) becomes NaN.
-      const int e = min(max(134 - static_cast<int>(big >> 7), -126), 126);
-      const float mul = big >= 0x7f80u ? __int_as_float(0x7fffffff)
-                                       : (big ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : 1.f);
-      uint32_t c1[4], c2[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x0 = __uint_as_float(w[2 * i] << 16) * mul, x1 = __uint_as_float(w[2 * i] & 0xffff0000u) * mul;
-        const float x2 = __uint_as_float(w[2 * i + 1] << 16) * mul;
-        const float x3 = __uint_as_float(w[2 * i + 1] & 0xffff0000u) * mul;
-        c1[i] = pack_e4m3x4(x0, x1, x2, x3);
-        float y0, y1, y2, y3;
-        e4m3x4_values(c1[i], y0, y1, y2, y3);
-        c2[i] = pack_e4m3x4(x0 - y0, x1 - y1, x2 - y2, x3 - y3);
-      }
-      // 16-byte chunk c of the row, where the swizzle of D-byte rows puts it.
-      const uint32_t at = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    // 16-byte chunk c of the row, where the swizzle of D-byte rows puts it.
+    const uint32_t at = D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    if (r < b1) {
       *reinterpret_cast<uint4*>(q1 + at) = make_uint4(c1[0], c1[1], c1[2], c1[3]);
       *reinterpret_cast<uint4*>(q1 + L::kQTerm + at) = make_uint4(c2[0], c2[1], c2[2], c2[3]);
       if (c == 0) fr[r] = 1.f / mul;
@@ -500,8 +492,13 @@ __device__ __forceinline__ void s_role8(const Dec8Params& p, uint32_t sbase, uin
     const int n = it.t1 - it.t0 + 1;
     const uint32_t qbuf = items & 1;
     if (items >= 2 && !w.wait_warp(bar(L::kQEmpty + qbuf), ((items >> 1) - 1) & 1, code | (L::kQEmpty + qbuf))) break;
-    prepare_q8<D, NR>(p, it, smem, qbuf);
-    if (leader) mbar_arrive(bar(L::kQFull + qbuf));
+    if (items == 0) {  // the softmax warps prepare the first item's, while they have nothing else to do
+      if (!w.wait_warp(bar(L::kQFull), 0, code | L::kQFull)) break;
+      tc_fence_after_sync();
+    } else {
+      prepare_q8<D, NR>(p, it, smem, qbuf, 0, NR);
+      if (leader) mbar_arrive(bar(L::kQFull + qbuf));
+    }
     const uint64_t qd = q_desc0 + ((qbuf * L::kQBuf) >> 4);
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
@@ -586,43 +583,6 @@ __device__ __forceinline__ void pv_role8(const Dec8Params& p, uint32_t sbase, co
 }
 
 // ------------------------------------------------------------ softmax
-// out = sum_s w_s O_s / sum_s w_s over the S partial results of `rows` rows from grow0, w_s =
-// 2^(lse2_s - max), four columns of a row per thread, in the order of the splits.
-template <int D>
-__device__ __noinline__ void merge_rows8(const Dec8Params& p, size_t grow0, int rows) {
-  constexpr int Q = D / 4;
-  const int S = p.num_splits;
-#pragma unroll 1
-  for (int t = threadIdx.x; t < rows * Q; t += kWg) {
-    const size_t row = grow0 + t / Q;
-    const int c = t % Q * 4;
-    const float* pl = p.part_lse + row * S;
-    const float* po = p.part_o + row * S * D + c;
-    float top = -INFINITY;
-#pragma unroll 16
-    for (int k = 0; k < S; ++k) top = fmaxf(top, __ldcg(pl + k));
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    float wsum = 0.f;
-    const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll 16
-    for (int k = 0; k < S; ++k) {   // a split that saw nothing wrote zeros and lse -inf
-      const float wgt = dec_exp2(__ldcg(pl + k) - base);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(po + static_cast<size_t>(k) * D));
-      wsum += wgt;
-      sum.x = fmaf(wgt, o.x, sum.x);
-      sum.y = fmaf(wgt, o.y, sum.y);
-      sum.z = fmaf(wgt, o.z, sum.z);
-      sum.w = fmaf(wgt, o.w, sum.w);
-    }
-    const float inv = wsum != 0.f ? 1.f / wsum : 0.f;
-    uint2 h;
-    h.x = attn_sm100_dec::dec_pack_bf16x2(sum.x * inv, sum.y * inv);
-    h.y = attn_sm100_dec::dec_pack_bf16x2(sum.z * inv, sum.w * inv);
-    *reinterpret_cast<uint2*>(p.out + row * D + c) = h;
-    if (c == 0) p.lse[row] = wsum != 0.f ? (top + __log2f(wsum)) * kLn2 : -INFINITY;
-  }
-}
-
 template <int D, int NR>
 __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbase, uint8_t* smem, uint32_t tmem,
                                               const Waiter8& w) {
@@ -681,6 +641,11 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
     const int n = it.t1 - it.t0 + 1;
     const uint32_t qbuf = items & 1;
     const float* fr = fr_all + qbuf * NR;
+    if (n > 0 && items == 0) {
+      prepare_q8<D, NR>(p, it, smem, 0, warp * (NR / 4), (warp + 1) * (NR / 4));
+      bar_or(kBar, kWg, false);
+      if (key == 0) mbar_arrive(bar(L::kQFull));
+    }
     if (n > 0) failed = !w.wait_warp(bar(L::kQFull + qbuf), (items >> 1) & 1, code | (L::kQFull + qbuf));
     else if (it.bad && key == 0) atomicCAS(p.err, 0, kDErrSeqLen | (it.b & 0xFFFFF));
     uint32_t mbuf = 0;  // which negm is current
@@ -696,9 +661,11 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
     const int all_hi = p.mask_kind == kDMaskFull ? it.L - 1 : it.L - p.Nq;
     const int all_lo = p.mask_kind == kDMaskWindow ? it.L - p.window : 0;
 
-    float l[NR];
+    // Pairs of rows share a 64-bit register: packed fp32 arithmetic halves the instructions of
+    // the tile loop, which bound it at 32 rows.
+    uint64_t l2[NR / 2];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) l[r] = 0.f;
+    for (int r = 0; r < NR / 2; ++r) l2[r] = 0;  // (+0.f, +0.f)
 #pragma unroll 1
     for (int j = 0; ok && j < n; ++j) {
       const uint32_t gi = g + j, sb = gi % L::kSBufs;
@@ -714,7 +681,8 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       failed |= !w.wait_warp(bar(L::kSFull + sb), (gi / L::kSBufs) & 1, code | (L::kSFull + sb));
       tc_fence_after_sync();
       // y_r = x_r + log2 c of this key and every row, -inf where the row does not see the key.
-      float y[NR];
+      const uint64_t ksl2 = f32x2_pack(ksl, ksl), lv2 = f32x2_pack(lv, lv);
+      uint64_t y2[NR / 2];
 #pragma unroll
       for (int ch = 0; ch < CH; ++ch) {
         const uint32_t s_addr = lane_addr + L::kSCol + sb * L::kSCols + ch * 16;
@@ -722,11 +690,13 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
         tmem_load_2x16cols(s_addr, s_addr + NR, s1, s2);
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const float4 f4 = *reinterpret_cast<const float4*>(fr + ch * 16 + i);
-          const float ff[4] = {f4.x, f4.y, f4.z, f4.w};
+          const ulonglong2 f4 = *reinterpret_cast<const ulonglong2*>(fr + ch * 16 + i);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            y[ch * 16 + i + k] = fmaf((__uint_as_float(s1[i + k]) + __uint_as_float(s2[i + k])) * ksl, ff[k], lv);
+          for (int k = 0; k < 4; k += 2) {
+            const uint64_t a = f32x2_pack(__uint_as_float(s1[i + k]), __uint_as_float(s1[i + k + 1]));
+            const uint64_t b = f32x2_pack(__uint_as_float(s2[i + k]), __uint_as_float(s2[i + k + 1]));
+            y2[(ch * 16 + i + k) / 2] = f32x2_fma(f32x2_mul(f32x2_add(a, b), ksl2), k ? f4.y : f4.x, lv2);
+          }
         }
       }
       if (!(base + kKeys - 1 <= all_hi && (base >= all_lo || base + kKeys <= it.sinks))) {
@@ -735,19 +705,25 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
         for (int r = 0; r < NR; ++r)
           hidden |= ((pos > row_hi[r]) | ((pos < row_lo[r]) & (pos >= it.sinks)) ? 1u : 0u) << r;
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
-          if (hidden & (1u << r)) y[r] = -INFINITY;
+        for (int r = 0; r < NR / 2; ++r) {
+          float a, b;
+          f32x2_unpack(y2[r], a, b);
+          y2[r] = f32x2_pack(hidden & (1u << (2 * r)) ? -INFINITY : a, hidden & (2u << (2 * r)) ? -INFINITY : b);
+        }
       }
-      // e = y - m + kTop, the exponents of the weights, unless some row's maximum has grown.
+      // y - m + kTop are the exponents of the weights, unless some row's maximum has grown.
       const float* negm = negm_all + mbuf * NR;
       bool grown = j == 0;  // an item's first tile sets the maxima
       if (j > 0) {
         float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < NR; r += 4) {
-          const float4 m4 = *reinterpret_cast<const float4*>(negm + r);
-          top = max3f(top, y[r] + m4.x, y[r + 1] + m4.y);
-          top = max3f(top, y[r + 2] + m4.z, y[r + 3] + m4.w);
+          const ulonglong2 m4 = *reinterpret_cast<const ulonglong2*>(negm + r);
+          float a, b, c, d;
+          f32x2_unpack(f32x2_add(y2[r / 2], m4.x), a, b);
+          f32x2_unpack(f32x2_add(y2[r / 2 + 1], m4.y), c, d);
+          top = max3f(top, a, b);
+          top = max3f(top, c, d);
         }
         grown = bar_or(kBar, kWg, failed || top > kTop + kGrow);
       }
@@ -762,7 +738,9 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
           int mine = 0;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int m = __reduce_max_sync(0xffffffffu, ordered(y[ch * 16 + i]));
+            float a, b;
+            f32x2_unpack(y2[(ch * 16 + i) / 2], a, b);
+            const int m = __reduce_max_sync(0xffffffffu, ordered(i & 1 ? b : a));
             if (lane == i) mine = m;
           }
           if (lane < 16) wmax[warp * NR + ch * 16 + lane] = unordered(mine);
@@ -785,7 +763,7 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
         negm = negm_all + mbuf * NR;
         if (j > 0) {
 #pragma unroll
-          for (int r = 0; r < NR; ++r) l[r] *= coef[r];
+          for (int r = 0; r < NR / 2; ++r) l2[r] = f32x2_mul(l2[r], *reinterpret_cast<const uint64_t*>(coef + 2 * r));
 #pragma unroll 1
           for (int c = 0; c < 3 * NR; c += 16) {
             uint32_t o[16];
@@ -803,16 +781,18 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       // bits), whose upper byte is an E5M2 number; what that leaves, likewise; the last
       // remainder rounded to nearest.
       const uint32_t p_addr = sbase + L::kPOff + key * 16;
+      const uint64_t ivs2 = f32x2_pack(ivs, ivs);
 #pragma unroll
       for (int ch = 0; ch < CH; ++ch) {
         uint32_t t1[8], t2[8], t3[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int r = ch * 16 + 2 * i;
-          const float2 m2 = *reinterpret_cast<const float2*>(negm + r);
-          const float a = dec_exp2(y[r] + m2.x), b = dec_exp2(y[r + 1] + m2.y);
-          l[r] = fmaf(a, ivs, l[r]);
-          l[r + 1] = fmaf(b, ivs, l[r + 1]);
+          const int r = ch * 8 + i;
+          float a, b;
+          f32x2_unpack(f32x2_add(y2[r], *reinterpret_cast<const uint64_t*>(negm + 2 * r)), a, b);
+          a = dec_exp2(a);
+          b = dec_exp2(b);
+          l2[r] = f32x2_fma(f32x2_pack(a, b), ivs2, l2[r]);
           const uint32_t h = pack_f16x2(a, b);
           t1[i] = h & 0xff00ff00u;
           const uint32_t r1 = half2_sub(h, t1[i]);
@@ -858,7 +838,7 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
     for (int ch = 0; ch < CH; ++ch) {
       float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = l[ch * 16 + i];
+      for (int i = 0; i < 8; ++i) f32x2_unpack(l2[ch * 8 + i], v[2 * i], v[2 * i + 1]);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) {
         const bool up = lane & o;
@@ -889,21 +869,35 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
     bar_or(kBar, kWg, false);
     // Thread = column of d.  An item without tiles has no O: its rows are zero (one split), or
     // carry no weight in the merge.
+    float* po = S > 1 ? p.part_o + (grow0 * S + it.s) * D + key : nullptr;
+    __nv_bfloat16* ob = p.out + grow0 * D + key;
+    const size_t po_step = static_cast<size_t>(S) * D;
 #pragma unroll 1
     for (int r0 = 0; r0 < it.rows; r0 += 16) {
       uint32_t o[16], o2[16], o3[16];
       const uint32_t at = lane_addr + L::kOCol + r0;
       tmem_load_16cols(at, o);
       tmem_load_2x16cols(at + NR, at + 2 * NR, o2, o3);
+      const int left = key < D ? it.rows - r0 : 0;
+      float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = r0 + i;
-        if (r < it.rows && key < D) {
-          float v = (__uint_as_float(o[i]) + (__uint_as_float(o2[i]) + __uint_as_float(o3[i]))) * coef[r];
-          if (n <= 0) v = 0.f;
-          if (S > 1) p.part_o[((grow0 + r) * S + it.s) * D + key] = v;
-          else p.out[(grow0 + r) * D + key] = __float2bfloat16_rn(v);
-        }
+      for (int i = 0; i < 16; i += 4) {
+        const float4 c4 = *reinterpret_cast<const float4*>(coef + r0 + i);
+        const float cc[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[i + k] = n <= 0 ? 0.f
+                            : (__uint_as_float(o[i + k]) + (__uint_as_float(o2[i + k]) + __uint_as_float(o3[i + k]))) *
+                                  cc[k];
+      }
+      if (po) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i, po += po_step)
+          if (i < left) *po = v[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i, ob += D)
+          if (i < left) *ob = __float2bfloat16_rn(v[i]);
       }
     }
     if (n > 0) {
@@ -912,20 +906,6 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       if (lane == 0) mbar_arrive(bar(L::kOFree));
       g += n;
       ++items;
-    }
-    if (p.done) {
-      // This item's partial result is written: the CTA whose item is the last of its unit to
-      // get here merges them all.
-      __threadfence();
-      bool last = false;
-      bar_or(kBar, kWg, false);
-      if (key == 0) {
-        unsigned int* count = p.done + it.unit;
-        last = atomicAdd(count, 1u) == static_cast<unsigned>(S - 1);
-        if (last) atomicExch(count, 0u);
-        __threadfence();
-      }
-      if (bar_or(kBar, kWg, last)) merge_rows8<D>(p, grow0, it.rows);
     }
     it = nx;
   }
@@ -941,6 +921,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode8_kernel(cons
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
   volatile uint32_t* loaded = reinterpret_cast<volatile uint32_t*>(smem + L::kMiscOff + 8);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be set up; it waits for this grid's end
   if (threadIdx.x == 0) {
     auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
     for (int i = 0; i < 2; ++i) {
@@ -1003,6 +984,100 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode8_kernel(cons
       atomicExch(p.sched + 1, 0u);
     }
   }
+}
+
+// ------------------------------------------------------------ split merge
+// One CTA per query row: out = sum_s w_s O_s / sum_s w_s, w_s = 2^(lse2_s - max lse2), lse = ln
+// sum_s 2^lse2_s.  Warp g takes splits g, g + 4, ..., a lane D / 32 columns; its first loads of O
+// are under way while the weights are formed.  Sums in a fixed order.
+struct Merge8Params {
+  const float* part_o;
+  const float* part_lse;
+  __nv_bfloat16* out;
+  float* lse;
+  int num_splits;
+};
+constexpr int kMergeBatch = 8;  // splits of a warp whose loads are in flight together
+
+template <int D>
+__global__ void __launch_bounds__(128) attn_decode8_merge_kernel(const Merge8Params p) {
+  constexpr int V = D / 32;
+  extern __shared__ float s_w[];  // [num_splits]
+  __shared__ float s_red[2][4], s_acc[3][D];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int S = p.num_splits;
+  const float* po = p.part_o + static_cast<size_t>(row) * S * D + lane * V;
+  float o[kMergeBatch][V];
+  auto load = [&](int first) {
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const int k = first + 4 * u;
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[u][v] = 0.f;
+      if (k < S) {
+        const float* src = po + static_cast<size_t>(k) * D;
+        if constexpr (V == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+          o[u][0] = x.x;
+          o[u][1] = x.y;
+          o[u][2] = x.z;
+          o[u][3] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          o[u][0] = x.x;
+          o[u][1] = x.y;
+        }
+      }
+    }
+  };
+  load(warp);
+  float top = -INFINITY;
+  for (int k = tid; k < S; k += 128) {
+    const float l2 = __ldcg(p.part_lse + static_cast<size_t>(row) * S + k);
+    s_w[k] = l2;
+    top = fmaxf(top, l2);
+  }
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+  if (lane == 0) s_red[0][warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3]));
+  const float base = top == -INFINITY ? 0.f : top;
+  float acc[V], wsum = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int k0 = warp;; ) {
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const int k = k0 + 4 * u;
+      const float w = k < S ? attn_sm100_dec::dec_exp2(s_w[k] - base) : 0.f;
+      wsum += w;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = fmaf(w, o[u][v], acc[v]);
+    }
+    k0 += 4 * kMergeBatch;
+    if (k0 >= S) break;
+    load(k0);
+  }
+  if (lane == 0) s_red[1][warp] = wsum;
+  if (warp > 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_acc[warp - 1][lane * V + v] = acc[v];
+  }
+  __syncthreads();
+  if (warp > 0) return;
+  wsum = (s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]);
+  const float inv = wsum != 0.f ? 1.f / wsum : 0.f;
+  __nv_bfloat16* dst = p.out + static_cast<size_t>(row) * D + lane * V;
+#pragma unroll
+  for (int v = 0; v < V; v += 2) {
+    const int c = lane * V + v;
+    const float a = ((acc[v] + s_acc[0][c]) + (s_acc[1][c] + s_acc[2][c])) * inv;
+    const float b = ((acc[v + 1] + s_acc[0][c + 1]) + (s_acc[1][c + 1] + s_acc[2][c + 1])) * inv;
+    *reinterpret_cast<uint32_t*>(dst + v) = attn_sm100_dec::dec_pack_bf16x2(a, b);
+  }
+  if (lane == 0) p.lse[row] = wsum != 0.f ? (top + __log2f(wsum)) * kLn2 : -INFINITY;
 }
 
 }  // namespace attn_sm100_dec8

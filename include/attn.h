@@ -519,9 +519,8 @@ int attn_kv_append_debug_error(cudaStream_t stream, int* device_code);
  *                     between the sinks and the oldest window position are neither looked up nor
  *                     read. Must be 0 with the other masks
  *   workspace         device, 16-byte aligned, attn_decode_kv8_workspace_bytes(B, Hq, Hkv, Nq, d,
- *                     num_splits) bytes, with the contract of attn_decode's, but that its first
- *                     65536 bytes are the counters that are zero before the first call and after
- *                     each (steps of other sizes may share it; not concurrent calls)
+ *                     num_splits) bytes, with the contract of attn_decode's (first 256 bytes zero
+ *                     before the first call and after each; not shared by concurrent calls)
  *   opts              wait bound and CTA count as for attn_fwd_ex; may be NULL
  *
  * Precision: the products take the codes exactly; a bf16 query row is split into two E4M3

@@ -222,14 +222,13 @@ def test_repeatable_and_workspace_left_clean(cuda_ok):
             got = attn.decode_kv8(s["q"], s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"], s["block_table"],
                                   s["seq_lens"], num_splits=splits, workspace=ws, grid_ctas=grid, out=out)
             torch.cuda.synchronize()
-            assert int(ws[:16384].view(torch.int32).abs().sum()) == 0     # the counters
+            assert int(ws[:64].view(torch.int32).abs().sum()) == 0     # the work counter
             first = first or [t.clone() for t in got]
             assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
 
 
 def test_one_workspace_for_steps_of_other_sizes_and_many_units(cuda_ok):
-    """A workspace serves steps of other sizes one after another, and a step of more units than
-    merge inside the kernel (17000 sequences of one head) equals the reference too."""
+    """A workspace serves steps of other sizes one after another; 17000 sequences of one head."""
     import exact_io_aware_72_b200 as attn
     B = 17000
     ws = attn.decode_kv8_workspace(B, 1, 1, 1, 64, 2)
@@ -238,7 +237,7 @@ def test_one_workspace_for_steps_of_other_sizes_and_many_units(cuda_ok):
         s = make(*args)
         out, lse = run(s, num_splits=splits, workspace=ws)
         compare(out, lse, reference(s), args[4])
-        assert int(ws[:16384].view(torch.int32).abs().sum()) == 0
+        assert int(ws[:64].view(torch.int32).abs().sum()) == 0
 
 
 def test_append_and_decode_run_together(cuda_ok):
