@@ -104,7 +104,7 @@ struct Dec8Params {
   int B, Hq, Hkv, Nq, group;
   int rows_total, rows_chunk, row_chunks;
   int page_size, page_shift, rows_per_load, loads_per_tile, max_pages, num_pages;
-  int block_shift, blocks_per_page;
+  int block_shift;
   int mask_kind, window, sinks;
   int num_splits, num_items;
   float scale_log2;
@@ -221,6 +221,14 @@ __device__ __noinline__ bool wait_long8(uint32_t bar, uint32_t parity, int code,
 }
 struct Waiter8 {
   const DecWaiter* w;
+  // This lane's answer, for the softmax warps, which agree on it at their next barrier (called
+  // by the whole warp, whatever its lanes have seen before).
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int code) const {
+    bool got = mbar_try_wait(bar, parity);
+    if (!got) got = wait_long8(bar, parity, code, w);
+    __syncwarp();
+    return got;
+  }
   __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, int code) const {
     bool got = mbar_try_wait(bar, parity);
     if (!__all_sync(0xffffffffu, got)) got = got || wait_long8(bar, parity, code, w);
@@ -241,8 +249,8 @@ __device__ __forceinline__ Item8 take_item8(uint32_t sbase, const uint8_t* smem,
     if ((threadIdx.x & 31) == 0) mbar_arrive(sbase + L::kBarOff + 8u * (L::kItemEmpty + slot));
     ++k;
   } else {
+    it = Item8{};
     it.idx = -1;
-    it.t0 = 0;
     it.t1 = -1;
   }
   return it;
@@ -341,8 +349,8 @@ __device__ __forceinline__ uint32_t loader8(const Dec8Params& p, uint32_t sbase,
       fetch();
       it = item8(p, idx);
     } else {
+      it = Item8{};
       it.idx = -2;
-      it.t0 = 0;
       it.t1 = -1;
     }
     if (lane == 0) {
@@ -604,21 +612,19 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
   bool failed = false;
 
   // What the threads of an item ask for ahead: the scales of this thread's key, loaded a tile
-  // ahead, and their page-table entry two tiles ahead.
+  // ahead, and their page-table entry two tiles ahead.  Where there is no such tile, or the
+  // step does not see the key, position 0 stands in: its weight is zero whatever is read.
+  const int hkv_block = p.page_shift - p.block_shift;
   auto pos_of = [&](const Item8& it, int j) -> int {
-    if (it.t0 + j > it.t1) return -1;
     const int pos = it.tile(it.t0 + j) * kKeys + key;
-    return it.seen(pos) ? pos : -1;
+    return it.t0 + j <= it.t1 && it.seen(pos) ? pos : 0;
   };
   auto entry_of = [&](const Item8& it, int pos) -> int {
-    return pos < 0 ? 0 : __ldg(p.block_table + static_cast<size_t>(it.b) * p.max_pages + (pos >> p.page_shift));
+    return __ldg(p.block_table + static_cast<size_t>(it.b) * p.max_pages + (pos >> p.page_shift));
   };
   auto scales_of = [&](const Item8& it, int pos, int entry, float& ks, float& vs) {
-    ks = 0.f;
-    vs = 1.f;
-    if (pos < 0) return;
-    const int page = (entry < 0 || entry >= p.num_pages) ? 0 : entry;
-    const size_t at = (static_cast<size_t>(page) * p.Hkv + it.hkv) * p.blocks_per_page +
+    const int page = static_cast<unsigned>(entry) < static_cast<unsigned>(p.num_pages) ? entry : 0;
+    const size_t at = (static_cast<size_t>(page * p.Hkv + it.hkv) << hkv_block) +
                       ((pos & (p.page_size - 1)) >> p.block_shift);
     ks = __ldg(p.k_scale + at);
     vs = __ldg(p.v_scale + at);
@@ -646,7 +652,7 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       bar_or(kBar, kWg, false);
       if (key == 0) mbar_arrive(bar(L::kQFull));
     }
-    if (n > 0) failed = !w.wait_warp(bar(L::kQFull + qbuf), (items >> 1) & 1, code | (L::kQFull + qbuf));
+    if (n > 0) failed = !w.wait(bar(L::kQFull + qbuf), (items >> 1) & 1, code | (L::kQFull + qbuf));
     else if (it.bad && key == 0) atomicCAS(p.err, 0, kDErrSeqLen | (it.b & 0xFFFFF));
     uint32_t mbuf = 0;  // which negm is current
     if (key < NR) {
@@ -678,7 +684,7 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       pos_next = pos_of(it, j + 2);
       entry_next = entry_of(it, pos_next);
       const int base = it.tile(it.t0 + j) * kKeys, pos = base + key;
-      failed |= !w.wait_warp(bar(L::kSFull + sb), (gi / L::kSBufs) & 1, code | (L::kSFull + sb));
+      failed |= !w.wait(bar(L::kSFull + sb), (gi / L::kSBufs) & 1, code | (L::kSFull + sb));
       tc_fence_after_sync();
       // y_r = x_r + log2 c of this key and every row, -inf where the row does not see the key.
       const uint64_t ksl2 = f32x2_pack(ksl, ksl), lv2 = f32x2_pack(lv, lv);
@@ -728,7 +734,7 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
         grown = bar_or(kBar, kWg, failed || top > kTop + kGrow);
       }
       // The last product has read P, and O may be changed.
-      if (!failed && gi > 0) failed = !w.wait_warp(bar(L::kPVDone), (gi - 1) & 1, code | L::kPVDone);
+      if (gi > 0) failed |= !w.wait(bar(L::kPVDone), (gi - 1) & 1, code | L::kPVDone);
       if (grown) {
         // Every warp's row maxima, then m and factor of every row: a row's m moves to its
         // maximum when that is more than kGrow above it.
@@ -811,7 +817,7 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       if (base + kKeys > it.L || (base < it.lo_pos && base + kKeys > it.sinks)) {
         // Rows of V that the step does not see were not loaded, or hold anything: zero them.
         const uint32_t slot = gi % L::kVSlots;
-        failed |= !w.wait_warp(bar(L::kVFull + slot), (gi / L::kVSlots) & 1, code | (L::kVFull + slot));
+        failed |= !w.wait(bar(L::kVFull + slot), (gi / L::kVSlots) & 1, code | (L::kVFull + slot));
         if (!failed && !it.seen(pos)) {
           const uint32_t at = sbase + L::kVOff + slot * L::kTileBytes + key * D;
 #pragma unroll
@@ -852,7 +858,7 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       if (lane < 16) wmax[warp * NR + ch * 16 + lane] = v[0];
     }
     if (n > 0) {
-      if (!failed) failed = !w.wait_warp(bar(L::kPVDone), (g + n - 1) & 1, code | L::kPVDone);
+      failed |= !w.wait(bar(L::kPVDone), (g + n - 1) & 1, code | L::kPVDone);
       if (lane == 0) mbar_arrive(bar(L::kQEmpty + qbuf));  // this warp has read the row factors
     }
     if (bar_or(kBar, kWg, failed)) break;
