@@ -20,8 +20,11 @@
 // takes one unit: the new tokens of one sequence that fall into one aligned run of `unit`
 // slots (a block, or 16 slots), so a block's largest magnitude is found inside one CTA, in
 // a fixed order, without atomics.  The unit's cos / sin table is computed once into shared
-// memory and used by all of the CTA's heads; the heads are dealt over gridDim.y when there
-// are few units.
+// memory; a group of D / 16 lanes takes a token's 16-element pieces of one head after another
+// with that token's cosines in registers, four heads' loads in flight.  (Rows dealt to the
+// groups head by head read the table anew for each, four lanes on a bank: 137 us instead of
+// 114 us for 16384 tokens of 64/8 heads.)  The heads are dealt over gridDim.y when there are
+// few units.
 #include "attn.h"
 
 #include <cuda_bf16.h>
@@ -172,8 +175,18 @@ __device__ __forceinline__ void chunk_at(const AppParams& p, int c, int& lo, int
   }
 }
 
+// The table's entry of token t and pair f: the pairs 8c + i of lanes c = 0, 1, ... are
+// neighbours, and tokens lie 64 bytes apart in the banks, so that the lanes of a warp read
+// without conflicts.
+__device__ __forceinline__ int cs_at(const AppParams& p, int t, int f) {
+  return t * (p.half + 8) + (f & 7) * (p.half / 8) + (f >> 3);
+}
+__device__ __forceinline__ void read_cs(const AppParams& p, const float2* table, int t, int c, float2 (&cs)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) cs[i] = table[cs_at(p, t, 8 * c + i)];
+}
 // Rotates a lane's 16 elements in place; cs = the token's (cos, sin) of pairs 8c .. 8c + 7.
-__device__ __forceinline__ void rotate16(bool interleaved, const float2* cs, float (&a)[8], float (&b)[8]) {
+__device__ __forceinline__ void rotate16(bool interleaved, const float2 (&cs)[8], float (&a)[8], float (&b)[8]) {
   if (!interleaved) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -200,24 +213,72 @@ __device__ __forceinline__ float block_scale(float amax) {
   const int e = static_cast<int>(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
   return __uint_as_float(static_cast<uint32_t>(max(e, -40) + 127) << 23);
 }
-__device__ __forceinline__ float finite_mag(float x) {
-  const float m = fabsf(x);
-  return m <= 3.402823466e38f ? m : 0.f;  // NaN and infinities do not set a scale
-}
-// Eight values to E4M3 codes of x / s.
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float s, float inv, bool pow2) {
-  float y[8];
+// Largest finite magnitude of a lane's 16 values: NaN and infinities do not set a scale.  (NaN
+// loses against any number; an infinity, rare, is taken out in a second look.)
+__device__ __forceinline__ float largest16(const float (&a)[8], const float (&b)[8]) {
+  float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = pow2 ? x[i] * inv : __fdiv_rn(x[i], s);
-  return make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
+  for (int i = 0; i < 8; ++i) m = max3f(m, fabsf(a[i]), fabsf(b[i]));
+  if (m > 3.402823466e38f) {
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = fabsf(a[i]), y = fabsf(b[i]);
+      m = max3f(m, x <= 3.402823466e38f ? x : 0.f, y <= 3.402823466e38f ? y : 0.f);
+    }
+  }
+  return m;
 }
-template <int D, bool FP8>
+// The division by a kept scale that is no power of two, which only a caller brings: out of line
+// (sixteen divisions in the row loop made it too large for the instruction cache).
+__device__ __noinline__ float quotient(float x, float s) { return __fdiv_rn(x, s); }
+// A lane's 16 values to E4M3 codes of x / s at two places; s is nearly always a power of two,
+// and x (1 / s) the quotient.
+__device__ __forceinline__ void encode16(float (&a)[8], float (&b)[8], float s, uint8_t* at_a, uint8_t* at_b) {
+  if ((__float_as_uint(s) & 0x7fffffu) == 0) {
+    const float inv = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] *= inv;
+      b[i] *= inv;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] = quotient(a[i], s);
+      b[i] = quotient(b[i], s);
+    }
+  }
+  *reinterpret_cast<uint2*>(at_a) =
+      make_uint2(pack_e4m3x4(a[0], a[1], a[2], a[3]), pack_e4m3x4(a[4], a[5], a[6], a[7]));
+  *reinterpret_cast<uint2*>(at_b) =
+      make_uint2(pack_e4m3x4(b[0], b[1], b[2], b[3]), pack_e4m3x4(b[4], b[5], b[6], b[7]));
+}
+// Sixteen codes in place, under a scale that is 1 / ratio times theirs.
+__device__ __forceinline__ void recode16(uint8_t* codes, float ratio) {
+  uint4* at = reinterpret_cast<uint4*>(codes);
+  const uint4 w = *at;
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x0, x1, x2, x3;
+    e4m3x4_values(in[i], x0, x1, x2, x3);
+    out[i] = pack_e4m3x4(x0 * ratio, x1 * ratio, x2 * ratio, x3 * ratio);
+  }
+  *at = make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// MODE 0: bf16 cache; 1, 2, 4: E4M3 cache with units of 16 MODE slots (smaller blocks are runs of a
+// unit of 16), a thread's pieces of a step in registers; 8: larger blocks, read twice.
+template <int D, int MODE>
 __global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_constant__ AppParams p) {
   constexpr int G = D / 16;                  // lanes of a row
   constexpr int kRows = kAppThreads / G;     // rows a pass of the CTA takes
-  extern __shared__ float2 s_cs[];           // [unit][half] (cos, sin) of the unit's tokens
+  extern __shared__ float2 s_cs[];           // (cos, sin) of the unit's tokens and pairs, see cs_at
   __shared__ Unit s_unit;
   __shared__ float s_amax[2][kAppThreads / 32];
+  __shared__ float s_row[2][2][kRows];       // largest magnitudes of a step's rows, in turn
   const int tid = threadIdx.x, lane = tid & 31;
   if (tid < 32) {
     const Unit u = find_unit(p, blockIdx.x, lane);
@@ -233,7 +294,7 @@ __global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_c
     const float r = static_cast<float>(turns - rint(turns));
     float sn, cn;
     sincospif(2.f * r, &sn, &cn);
-    s_cs[i] = make_float2(cn, sn);
+    s_cs[cs_at(p, t, f)] = make_float2(cn, sn);
   }
   __syncthreads();
   const int c = tid % G, g = tid / G;
@@ -242,53 +303,164 @@ __global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_c
   const bool turn = 8 * c < p.half;
   const int parts = gridDim.y, part = blockIdx.y;
 
+  // Groups of lanes: `nt` tokens at a time (a power of two), kRows / nt groups for each.
+  int nt = 1;
+  while (nt < kRows && nt < u.n) nt *= 2;
+  const int tg = g % nt, hg = g / nt, hstep = kRows / nt;
+  // Rows (t, h), h0 <= h < h1, of one tensor: src_of and dst_of give a row's place.
+  auto sweep = [&](int h0, int h1, bool rotate, auto src_of, auto dst_of) {
+    for (int t = tg; t < u.n; t += nt) {
+      float2 cs[8];
+      if (rotate) read_cs(p, s_cs, t, c, cs);
+      for (int h = h0 + hg; h < h1; h += 4 * hstep) {
+        uint4 lo[4], hi[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (h + k * hstep < h1) {
+            const __nv_bfloat16* src = src_of(t, h + k * hstep);
+            lo[k] = __ldg(reinterpret_cast<const uint4*>(src + at_lo));
+            hi[k] = __ldg(reinterpret_cast<const uint4*>(src + at_hi));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (h + k * hstep < h1) {
+            if (rotate) {
+              float a[8], b[8];
+              widen8(lo[k], a);
+              widen8(hi[k], b);
+              rotate16(p.interleaved, cs, a, b);
+              lo[k] = narrow8(a);
+              hi[k] = narrow8(b);
+            }
+            __nv_bfloat16* dst = dst_of(t, h + k * hstep);
+            *reinterpret_cast<uint4*>(dst + at_lo) = lo[k];
+            *reinterpret_cast<uint4*>(dst + at_hi) = hi[k];
+          }
+        }
+      }
+    }
+  };
+
   // Queries: rotated into the decoding step's layout [B, Hq, Nq, d] (equal sequences) or
   // left token-major.
   if (p.q) {
     const int h0 = static_cast<int>(static_cast<int64_t>(p.Hq) * part / parts);
     const int h1 = static_cast<int>(static_cast<int64_t>(p.Hq) * (part + 1) / parts);
-    const int rows = u.n * (h1 - h0);
-    for (int r = g; r < rows; r += kRows) {
-      const int t = r / (h1 - h0), h = h0 + r - t * (h1 - h0);
-      const __nv_bfloat16* src = p.q + (u.t0 + t) * p.q_stride + h * D;
-      float a[8], b[8];
-      widen8(__ldg(reinterpret_cast<const uint4*>(src + at_lo)), a);
-      widen8(__ldg(reinterpret_cast<const uint4*>(src + at_hi)), b);
-      if (turn) rotate16(p.interleaved, s_cs + t * p.half + 8 * c, a, b);
-      const int64_t row = p.per_seq
-                              ? (static_cast<int64_t>(u.b) * p.Hq + h) * p.per_seq + (u.t0 + t - u.first)
-                              : static_cast<int64_t>(u.t0 + t) * p.Hq + h;
-      __nv_bfloat16* dst = p.q_out + row * D;
-      *reinterpret_cast<uint4*>(dst + at_lo) = narrow8(a);
-      *reinterpret_cast<uint4*>(dst + at_hi) = narrow8(b);
-    }
+    const int64_t row0 = p.per_seq ? static_cast<int64_t>(u.b) * p.Hq * p.per_seq + (u.t0 - u.first)
+                                   : static_cast<int64_t>(u.t0) * p.Hq;
+    const int64_t row_t = p.per_seq ? 1 : p.Hq, row_h = p.per_seq ? p.per_seq : 1;
+    sweep(h0, h1, turn, [&](int t, int h) { return p.q + (u.t0 + t) * p.q_stride + h * D; },
+          [&](int t, int h) { return p.q_out + (row0 + t * row_t + h * row_h) * D; });
   }
   if (u.page < 0) return;
   const int h0 = static_cast<int>(static_cast<int64_t>(p.Hkv) * part / parts);
   const int h1 = static_cast<int>(static_cast<int64_t>(p.Hkv) * (part + 1) / parts);
-  if constexpr (!FP8) {
-    const int rows = u.n * (h1 - h0) * 2;
-    for (int r = g; r < rows; r += kRows) {
-      const int kv = r & 1, i = r >> 1;
-      const int t = i / (h1 - h0), h = h0 + i - t * (h1 - h0);
-      const __nv_bfloat16* src = (kv ? p.v + (u.t0 + t) * p.v_stride : p.k + (u.t0 + t) * p.k_stride) + h * D;
-      uint4 lo = __ldg(reinterpret_cast<const uint4*>(src + at_lo));
-      uint4 hi = __ldg(reinterpret_cast<const uint4*>(src + at_hi));
-      if (!kv && turn) {
-        float a[8], b[8];
-        widen8(lo, a);
-        widen8(hi, b);
-        rotate16(p.interleaved, s_cs + t * p.half + 8 * c, a, b);
-        lo = narrow8(a);
-        hi = narrow8(b);
+  if constexpr (MODE == 0) {
+    for (int kv = 0; kv < 2; ++kv) {
+      const __nv_bfloat16* base = kv ? p.v : p.k;
+      const int64_t stride = kv ? p.v_stride : p.k_stride;
+      __nv_bfloat16* cache = static_cast<__nv_bfloat16*>(kv ? p.v_cache : p.k_cache) +
+                             (u.page * p.Hkv * p.page_size + u.in_page + u.slot0) * D;
+      sweep(h0, h1, !kv && turn, [&](int t, int h) { return base + (u.t0 + t) * stride + h * D; },
+            [&](int t, int h) { return cache + (static_cast<int64_t>(h) * p.page_size + t) * D; });
+    }
+  } else if constexpr (MODE <= 4) {
+    // Half of the CTA takes K and half V; a group of lanes takes slots slot, slot + 16, ... of
+    // the unit, one or two heads a step (with d = 64, every other head).  The largest magnitudes of
+    // a step go to shared memory, and a block's is the largest of its rows': one barrier a step.
+    constexpr int kPass = kRows / 2, kHeads = kPass / 16, kStep = MODE == 1 ? 2 : 1;
+    const int kv = g / kPass, slot = g % kPass % 16, hs = g % kPass / 16;
+    const __nv_bfloat16* base = (kv ? p.v : p.k);
+    const int64_t stride = kv ? p.v_stride : p.k_stride;
+    float* scales = kv ? p.v_scale : p.k_scale;
+    const int blocks_per_page = p.page_size / p.block;
+    const int b0 = MODE == 1 ? slot / p.block * p.block : 0;  // this thread's block: its first slot,
+    const int first = max(b0, u.slot0);                       // its first new one,
+    const bool has_new = b0 + p.block > u.slot0 && b0 < u.slot0 + u.n;
+    const bool held = has_new && first > b0;                  // and whether it held tokens before
+    auto fresh = [&](int r) { return slot + 16 * r >= u.slot0 && slot + 16 * r < u.slot0 + u.n; };
+    const bool rotate = !kv && turn;
+    float2 cs[8];
+    if (MODE == 1 && rotate && fresh(0)) read_cs(p, s_cs, slot - u.slot0, c, cs);
+    const __nv_bfloat16* src = base + (u.t0 + slot - u.slot0) * stride;
+    uint8_t* rows = static_cast<uint8_t*>(kv ? p.v_cache : p.k_cache) +
+                    (u.page * p.Hkv * p.page_size + u.in_page + slot) * D;
+    auto values = [&](const uint4& lo, const uint4& hi, int r, float (&a)[8], float (&b)[8]) {
+      widen8(lo, a);
+      widen8(hi, b);
+      if (rotate) {
+        if (MODE > 1) read_cs(p, s_cs, slot + 16 * r - u.slot0, c, cs);
+        rotate16(p.interleaved, cs, a, b);
       }
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(kv ? p.v_cache : p.k_cache) +
-                           ((u.page * p.Hkv + h) * p.page_size + u.in_page + u.slot0 + t) * D;
-      *reinterpret_cast<uint4*>(dst + at_lo) = lo;
-      *reinterpret_cast<uint4*>(dst + at_hi) = hi;
+    };
+    int par = 0;
+#pragma unroll 1
+    for (int hb = h0 + hs; hb - hs < h1; hb += kStep * kHeads, par ^= 1) {
+      uint4 lo[kStep][MODE], hi[kStep][MODE];
+      float old[kStep];
+#pragma unroll
+      for (int q = 0; q < kStep; ++q) {
+        const int h = hb + q * kHeads;
+        old[q] = 0.f;
+        if (held && h < h1)
+          old[q] = scales[(u.page * p.Hkv + h) * blocks_per_page + (u.in_page + b0) / p.block];
+#pragma unroll
+        for (int r = 0; r < MODE; ++r) {
+          if (h < h1 && fresh(r)) {
+            lo[q][r] = __ldg(reinterpret_cast<const uint4*>(src + 16 * r * stride + h * D + at_lo));
+            hi[q][r] = __ldg(reinterpret_cast<const uint4*>(src + 16 * r * stride + h * D + at_hi));
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kStep; ++q) {
+        float amax = 0.f;
+#pragma unroll
+        for (int r = 0; r < MODE; ++r) {
+          if (hb + q * kHeads < h1 && fresh(r)) {
+            float a[8], b[8];
+            values(lo[q][r], hi[q][r], r, a, b);
+            amax = fmaxf(amax, largest16(a, b));
+          }
+        }
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (c == 0) s_row[par][q][g] = amax;
+      }
+      __syncthreads();  // (also: every thread has read the old scales)
+#pragma unroll
+      for (int q = 0; q < kStep; ++q) {
+        const int h = hb + q * kHeads;
+        if (!has_new || h >= h1) continue;
+        float amax = 0.f;
+        const float* rowmax = &s_row[par][q][g - slot + b0];
+        if (MODE > 1 || p.block == 16) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) amax = fmaxf(amax, rowmax[r]);
+        } else {
+          for (int r = 0; r < p.block; ++r) amax = fmaxf(amax, rowmax[r]);
+        }
+        const bool keep = held && old[q] >= 1.17549435e-38f && amax <= 448.f * old[q];
+        const float s = keep ? old[q] : block_scale(amax);
+        uint8_t* dst = rows + static_cast<int64_t>(h) * p.page_size * D;
+#pragma unroll
+        for (int r = 0; r < MODE; ++r) {
+          if (fresh(r)) {
+            float a[8], b[8];
+            values(lo[q][r], hi[q][r], r, a, b);
+            encode16(a, b, s, dst + 16 * r * D + at_lo, dst + 16 * r * D + at_hi);
+          } else if (!keep && slot + 16 * r < u.slot0) {
+            recode16(dst + 16 * r * D + 16 * c, old[q] / s);
+          }
+          if (!keep && c == 0 && slot + 16 * r == first)
+            scales[(u.page * p.Hkv + h) * blocks_per_page + (u.in_page + b0) / p.block] = s;
+        }
+      }
     }
   } else {
-    // The unit's blocks one after another; in a block, half of the CTA takes K and half V.
+    // One block; half of the CTA takes K and half V, and each head's rows are read twice, for the
+    // largest magnitude and for the codes.
     constexpr int kPass = kRows / 2;
     const int kv = g / kPass, r0 = g - kv * kPass;
     const __nv_bfloat16* base = kv ? p.v : p.k;
@@ -300,7 +472,11 @@ __global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_c
       const __nv_bfloat16* src = base + (u.t0 + t) * stride + h * D;
       widen8(__ldg(reinterpret_cast<const uint4*>(src + at_lo)), a);
       widen8(__ldg(reinterpret_cast<const uint4*>(src + at_hi)), b);
-      if (!kv && turn) rotate16(p.interleaved, s_cs + t * p.half + 8 * c, a, b);
+      if (!kv && turn) {
+        float2 cs[8];
+        read_cs(p, s_cs, t, c, cs);
+        rotate16(p.interleaved, cs, a, b);
+      }
     };
     for (int h = h0; h < h1; ++h) {
       for (int s0 = u.slot0 / p.block * p.block; s0 < u.slot0 + u.n; s0 += p.block) {
@@ -310,8 +486,7 @@ __global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_c
         for (int t = ta + r0; t < tb; t += kPass) {
           float a[8], b[8];
           load(t, h, a, b);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(finite_mag(a[i]), finite_mag(b[i])));
+          amax = fmaxf(amax, largest16(a, b));
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -328,31 +503,16 @@ __global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_c
         const bool keep = held && old >= 1.17549435e-38f && amax <= 448.f * old;
         const float s = keep ? old : block_scale(amax);
         uint8_t* rows = cache + (head * p.page_size + u.in_page) * D;
-        const float inv = 1.f / s;
-        const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
         for (int t = ta + r0; t < tb; t += kPass) {
           float a[8], b[8];
           load(t, h, a, b);
           uint8_t* dst = rows + (u.slot0 + t) * D;
-          *reinterpret_cast<uint2*>(dst + at_lo) = encode8(a, s, inv, pow2);
-          *reinterpret_cast<uint2*>(dst + at_hi) = encode8(b, s, inv, pow2);
+          encode16(a, b, s, dst + at_lo, dst + at_hi);
         }
         if (held && !keep) {
           // Codes that were here before, under the new scale.
           const float ratio = old / s;
-          for (int r = r0; r < held; r += kPass) {
-            uint4* at = reinterpret_cast<uint4*>(rows + (s0 + r) * D + 16 * c);
-            const uint4 w = *at;
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-            uint32_t out[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float x0, x1, x2, x3;
-              e4m3x4_values(in[i], x0, x1, x2, x3);
-              out[i] = pack_e4m3x4(x0 * ratio, x1 * ratio, x2 * ratio, x3 * ratio);
-            }
-            *at = make_uint4(out[0], out[1], out[2], out[3]);
-          }
+          for (int r = r0; r < held; r += kPass) recode16(rows + (s0 + r) * D + 16 * c, ratio);
         }
         if (held) __syncthreads();  // every thread has read the old scale
         if (!keep && r0 == 0 && c == 0) *sc = s;
@@ -377,10 +537,22 @@ struct AppDevice {
 std::mutex g_app_mutex;
 AppDevice g_app_dev[kMaxDevices];
 
-template <int D, bool FP8>
+template <int D, int MODE>
 bool allow_smem(int bytes) {
-  return cudaFuncSetAttribute(attn_append_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+  return cudaFuncSetAttribute(attn_append_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
          cudaSuccess;
+}
+
+template <int D>
+cudaError_t launch_append(const AppParams& p, int mode, dim3 grid, size_t smem, cudaStream_t stream) {
+  switch (mode) {
+    case 0: attn_append_kernel<D, 0><<<grid, kAppThreads, smem, stream>>>(p); break;
+    case 1: attn_append_kernel<D, 1><<<grid, kAppThreads, smem, stream>>>(p); break;
+    case 2: attn_append_kernel<D, 2><<<grid, kAppThreads, smem, stream>>>(p); break;
+    case 4: attn_append_kernel<D, 4><<<grid, kAppThreads, smem, stream>>>(p); break;
+    default: attn_append_kernel<D, 8><<<grid, kAppThreads, smem, stream>>>(p); break;
+  }
+  return cudaGetLastError();
 }
 
 int app_device_setup(AppDevice& out) {
@@ -401,8 +573,8 @@ int app_device_setup(AppDevice& out) {
       void* addr = nullptr;
       if (cudaGetSymbolAddress(&addr, g_attn_app_error) != cudaSuccess) return ATTN_ERR_CUDA;
       info.err_word = static_cast<int*>(addr);
-      // a unit of 256 slots: 256 x d/2 pairs of 8 bytes
-      if (!allow_smem<64, true>(256 * 32 * 8) || !allow_smem<128, true>(256 * 64 * 8)) return ATTN_ERR_CUDA;
+      // a unit of 256 slots: 256 x (d/2 + 8) entries of 8 bytes
+      if (!allow_smem<64, 8>(256 * 40 * 8) || !allow_smem<128, 8>(256 * 72 * 8)) return ATTN_ERR_CUDA;
     }
     info.probed = true;
   }
@@ -514,18 +686,21 @@ extern "C" int attn_kv_append(const attn_kv_append_args* a, cudaStream_t stream)
     units = (a->T + p.unit - 1) / p.unit + std::min<int64_t>(a->B, a->T) * 2;
   }
   if (units > lim) return ATTN_ERR_INVALID_ARG;
-  // Few units: the heads are dealt over several CTAs of a unit, up to about two CTAs per SM.
-  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(a->Hkv, 2 * dev.sm_count / units));
+  // Few units: the heads are dealt evenly over several CTAs of a unit, up to about two CTAs per
+  // SM.  (Four per SM: 15.5 us instead of 10.4 for 2048 tokens of 32/8 heads; each CTA computes its
+  // unit's cosines.)  Small blocks of codes are split in two up to four units per SM, whose
+  // second wave would be nearly empty: 49 us instead of 54 for 8191 tokens.
+  const int64_t want = std::max<int64_t>(fp8 && p.unit == 16 && units < 4 * dev.sm_count ? 2 : 1,
+                                         2 * dev.sm_count / units);
+  const int64_t part_heads = std::max<int64_t>(1, a->Hkv / want);
+  const int64_t parts = std::min<int64_t>((a->Hkv + part_heads - 1) / part_heads, 65535);
   const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>(parts));
-  const size_t smem = static_cast<size_t>(p.unit) * p.half * sizeof(float2);
-  if (a->d == 64) {
-    if (fp8) attn_append_kernel<64, true><<<grid, kAppThreads, smem, stream>>>(p);
-    else attn_append_kernel<64, false><<<grid, kAppThreads, smem, stream>>>(p);
-  } else {
-    if (fp8) attn_append_kernel<128, true><<<grid, kAppThreads, smem, stream>>>(p);
-    else attn_append_kernel<128, false><<<grid, kAppThreads, smem, stream>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  const size_t smem = static_cast<size_t>(p.unit) * (p.half + 8) * sizeof(float2);
+  const int mode = fp8 ? std::min(p.unit / 16, 8) : 0;
+  return (a->d == 64 ? launch_append<64>(p, mode, grid, smem, stream)
+                     : launch_append<128>(p, mode, grid, smem, stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
 }
 
 extern "C" int attn_kv_append_debug_error(cudaStream_t stream, int* device_code) {

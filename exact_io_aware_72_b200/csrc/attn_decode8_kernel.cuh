@@ -13,7 +13,7 @@
 // so the value scale is folded into the weight that the P V product takes, and the running
 // maximum m is that of y.
 //
-// * S^T = K Q^T (128 keys x NR query rows, NR in {16, 32, 64}): an SS product with the K
+// * S^T = K Q^T (128 keys x NR query rows, NR = 16 or 32): an SS product with the K
 //   tile as A and Q as B.  bf16 q has 8 significant bits and E4M3 holds 4, so each q row,
 //   scaled by a power of two to a maximum in [128, 256), is the sum of two E4M3 numbers:
 //   the rounded value and the rest, which fits 4 bits exactly (elements below 2^-10 of the
