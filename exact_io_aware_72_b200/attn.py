@@ -6,6 +6,7 @@ fallback: if the library is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -194,6 +195,21 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float
     if st != 0:
         raise AttnError(st, "attn_fwd")
     return out, lse
+
+
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on_device(index: int):
+    """Context with device ``index`` current: nothing to enter where it is already (a decoding
+    step's call lasts some 10 us, and a switch and back costs 3 of them)."""
+    return _NO_SWITCH if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+def _stream_handle(stream: Optional[torch.cuda.Stream], index: int) -> int:
+    """``stream``'s handle, or the current stream's of device ``index`` (without the Stream object
+    around it, 5 us)."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _codes(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -494,33 +510,30 @@ def decode_kv8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
     if num_splits is None:
         num_splits = decode_kv8_num_splits(B, Hq, Hkv, Nq, max_pages * page_size if max_seq_len is None else max_seq_len,
                                            mask, window, sinks)
-    device = q.device
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
+        lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
     _check(out, "out", torch.bfloat16, 4)
     _check(lse, "lse", torch.float32, 3)
     if out.shape != q.shape or tuple(lse.shape) != (B, Hq, Nq):
         raise ValueError("out or lse has the wrong shape")
     if workspace is None:
-        workspace = decode_kv8_workspace(B, Hq, Hkv, Nq, d, num_splits, device)
+        workspace = decode_kv8_workspace(B, Hq, Hkv, Nq, d, num_splits, q.device)
     if not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    if any(t.device != device for t in (k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse,
-                                        workspace)):
-        raise ValueError("all tensors must be on one device")
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
+    index = q.get_device()
+    for t in (k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse, workspace):
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on one device")
     opts = FwdOptions(int(wait_timeout_ns), 0, int(grid_ctas))
-    with torch.cuda.device(device):
+    with _on_device(index):
         st = lib.attn_decode_kv8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                                  v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
-                                 lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                 B, Hq, Hkv, Nq, d, num_pages, page_size, max_pages, page_size // per_page,
-                                 int(num_splits), float(scale), MASKS[mask],
-                                 int(window) if window is not None else 0, int(sinks),
-                                 ctypes.c_void_p(stream.cuda_stream), ctypes.byref(opts))
+                                 lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, B, Hq, Hkv, Nq, d,
+                                 num_pages, page_size, max_pages, page_size // per_page, int(num_splits),
+                                 float(scale), MASKS[mask], int(window) if window is not None else 0, int(sinks),
+                                 _stream_handle(stream, index), ctypes.byref(opts))
     if st != 0:
         raise AttnError(st, "attn_decode_kv8")
     return out, lse
@@ -623,7 +636,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         given.append(q)
         shape = (T, q.shape[1], d) if cu_tokens is not None else (B, q.shape[1], T // B, d)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+            q_out = q.new_empty(shape)
         _check(q_out, "q_out", torch.bfloat16, len(shape))
         if tuple(q_out.shape) != shape:
             raise ValueError("q_out has the wrong shape")
@@ -631,13 +644,12 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         a.q_out = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    device = k.device
-    if any(t.device != device for t in given):
-        raise ValueError("all tensors must be on one device")
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    with torch.cuda.device(device):
-        st = lib.attn_kv_append(ctypes.byref(a), ctypes.c_void_p(stream.cuda_stream))
+    index = k.get_device()
+    for t in given:
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on one device")
+    with _on_device(index):
+        st = lib.attn_kv_append(ctypes.byref(a), _stream_handle(stream, index))
     if st != 0:
         raise AttnError(st, "attn_kv_append")
     return q_out
