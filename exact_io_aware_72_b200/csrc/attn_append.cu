@@ -6,8 +6,8 @@
 // Rotation of a pair (a, b) at position x with frequency f: (a c - b s, b c + a s) with
 // c = cos(x f), s = sin(x f).  An angle of a far position (2^17 and more) needs more bits
 // than fp32 has: x f is formed in fp64 as turns, x f / 2 pi, whose distance from the
-// nearest whole turn (at most a half) goes to fp32, so cos and sin are good to about one
-// fp32 rounding at every position.  The rotation itself is fp32, rounded once (to bf16, or
+// nearest whole turn (at most a half) goes to fp32, and what that rounding loses turns the result
+// once more, so cos and sin are good to about one fp32 rounding at every position.  The rotation itself is fp32, rounded once (to bf16, or
 // to the E4M3 code).
 //
 // Scales are powers of two (the smallest s >= 2^-40 with amax <= 448 s): E4M3 is a floating
@@ -291,10 +291,12 @@ __global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_c
     const int t = i / p.half, f = i - t * p.half;
     const int pos = p.positions ? __ldg(p.positions + u.t0 + t) : u.pos0 + t;
     const double turns = static_cast<double>(pos) * static_cast<double>(__ldg(p.inv_freq + f)) * 0.15915494309189535;
-    const float r = static_cast<float>(turns - rint(turns));
+    const double part = turns - rint(turns);
+    const float r = static_cast<float>(part);
+    const float rest = static_cast<float>((part - r) * 6.283185307179586);  // radians that r lost
     float sn, cn;
     sincospif(2.f * r, &sn, &cn);
-    s_cs[cs_at(p, t, f)] = make_float2(cn, sn);
+    s_cs[cs_at(p, t, f)] = make_float2(fmaf(-sn, rest, cn), fmaf(cn, rest, sn));
   }
   __syncthreads();
   const int c = tid % G, g = tid / G;
