@@ -260,6 +260,7 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
   p.sink_tiles = static_cast<int>(sink.tiles);
   p.sink_parts = static_cast<int>(sink.parts);
   p.part = sink.bytes ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_off) : nullptr;
+  p.part_unit = fused ? held_p_unit<false>() : held_p_unit<true>();
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.num_blk = static_cast<int>((N + kTile - 1) / kTile);

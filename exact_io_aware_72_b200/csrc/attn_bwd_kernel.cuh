@@ -78,6 +78,7 @@ struct BwdParams {
   int sink_tiles;     // ceil(sinks / 128)
   int sink_parts;     // items that a sink tile's queries are cut into (see DkvItem)
   float* part;        // sink_parts > 1: [B*Hkv][sink_tiles][sink_parts][dV, dK][128, d] fp32 sums
+  float part_unit;    // ... in units of this
   float scale;        // softmax scale (dQ, dK are scaled by it)
   float scale_log2;   // scale * log2(e)
   int num_blk;        // ceil(N / 128)
@@ -196,9 +197,16 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
 }
 
 // P between S and dP in the full-tile kernels: two values in a word.  The SINK kernels hold
-// fp16 (11 significant bits: P is at most 1) so that dS carries its own bf16 rounding alone;
-// the others hold the bf16 that the dV product takes, which adds as much again to dS (dq and
-// dk off by 2.9e-3 of their norm instead of 2.4e-3).
+// fp16 (11 significant bits) so that dS carries its own bf16 rounding alone; the others hold the
+// bf16 that the dV product takes, which adds as much again to dS (dq and dk off by 2.9e-3 of
+// their norm instead of 2.4e-3).  fp16's range is short: what is held, and with it dS and the
+// sums, is 2^kPShift P (P is at most 1, up to its fp32 rounding), which has all its bits down to
+// P = 2^-28; the factor is taken back where a row is stored.
+constexpr int kPShift = 14;
+template <bool SINK>
+__host__ __device__ __forceinline__ constexpr float held_p_unit() {
+  return SINK ? 1.f / (1 << kPShift) : 1.f;
+}
 template <bool SINK>
 __device__ __forceinline__ uint32_t hold_p(float lo, float hi) {
   return SINK ? pack_f16x2(lo, hi) : bf16x2_rn(lo, hi);
@@ -913,7 +921,8 @@ __device__ __forceinline__ void dqf_elem(const BwdParams& p, uint32_t sbase, uin
     const size_t bhrow = (static_cast<size_t>(it.b) * p.Hq + it.hq) * p.N + (row_ok ? row : 0);
     const float lse2 = row_ok ? p.lse[bhrow] * kLog2e : 0.f;
     const float dlt = row_ok ? p.delta[bhrow] : 0.f;
-    const uint64_t c2x2 = f32x2_pack(c2, c2), nlse2x2 = f32x2_pack(-lse2, -lse2), ndlt2 = f32x2_pack(-dlt, -dlt);
+    const float nlse = (SINK ? kPShift : 0) - lse2;
+    const uint64_t c2x2 = f32x2_pack(c2, c2), nlse2x2 = f32x2_pack(nlse, nlse), ndlt2 = f32x2_pack(-dlt, -dlt);
     bool ok = true;
     for (int u = it.lo - it.ns; u <= it.hi && ok; ++u, ++g) {
       const int j = it.tile(u);
@@ -985,7 +994,7 @@ __device__ __forceinline__ void dqf_elem(const BwdParams& p, uint32_t sbase, uin
     if (!ok) break;
     if (!w.wait_warp(bar(L::kAccDone), items & 1, code | L::kAccDone)) break;
     tc_fence_after_sync();
-    store_acc_row<D>(t_acc, p.scale, p.dq + bhrow * D, row_ok);
+    store_acc_row<D>(t_acc, p.scale * held_p_unit<SINK>(), p.dq + bhrow * D, row_ok);
     tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(L::kAccFree));
@@ -1143,7 +1152,7 @@ __device__ __forceinline__ void dkvf_elem(const BwdParams& p, uint32_t sbase, ui
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const int c = lane + 32 * t;
-          s_lse[c] = -s_lse[c] * kLog2e;
+          s_lse[c] = (SINK ? kPShift : 0) - s_lse[c] * kLog2e;
           s_dlt[c] = -s_dlt[c];
         }
         __syncwarp();
@@ -1247,8 +1256,8 @@ __device__ __forceinline__ void dkvf_elem(const BwdParams& p, uint32_t sbase, ui
       store_acc_row_f32<D>(t_dv, dst);
       store_acc_row_f32<D>(t_dk, dst + kTile * D);
     } else {
-      store_acc_row<D>(t_dv, 1.f, p.dv + krow * D, key_ok);
-      store_acc_row<D>(t_dk, p.scale, p.dk + krow * D, key_ok);
+      store_acc_row<D>(t_dv, held_p_unit<SINK>(), p.dv + krow * D, key_ok);
+      store_acc_row<D>(t_dk, p.scale * held_p_unit<SINK>(), p.dk + krow * D, key_ok);
     }
     tc_fence_before_sync();
     __syncwarp();
@@ -1338,7 +1347,7 @@ __global__ void __launch_bounds__(256) attn_bwd_sink_reduce_kernel(const __grid_
     sum.z += x.z;
     sum.w += x.w;
   }
-  const float mul = which ? p.scale : 1.f;
+  const float mul = which ? p.scale * p.part_unit : p.part_unit;
   __nv_bfloat16* dst = (which ? p.dk : p.dv) + (static_cast<size_t>(bk) * p.N + key) * D + c;
   *reinterpret_cast<uint2*>(dst) = make_uint2(bf16x2_rn(sum.x * mul, sum.y * mul), bf16x2_rn(sum.z * mul, sum.w * mul));
 }

@@ -85,7 +85,7 @@ constexpr int kItemSlots = 4;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTop = 9.f;      // weights at the running maximum are 2^kTop
 constexpr float kGrow = 6.f;     // the running maximum moves when a row's grows by more
-constexpr float kNoMax = -1e30f; // running maximum of a row that has seen no key
+constexpr float kNoMax = -3e38f; // running maximum of a row that has seen no key
 constexpr float kScaleMin = 9.094947017729282e-13f, kScaleMax = 1099511627776.f;  // 2^-40, 2^40
 
 struct Dec8Params {
