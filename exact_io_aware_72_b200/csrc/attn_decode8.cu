@@ -153,14 +153,21 @@ extern "C" int64_t attn_decode_kv8_num_splits(int64_t B, int64_t Hq, int64_t Hkv
   const int64_t chunks = (rows_total + kMaxRows - 1) / kMaxRows;
   const int64_t units = B * Hkv * chunks;
   int64_t tiles = (max_seq_len + kKeys - 1) / kKeys + 1;
-  if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window < max_seq_len)
+  const bool windowed = mask_kind == ATTN_MASK_SLIDING_WINDOW && window < max_seq_len;
+  if (windowed)
     tiles = std::min(tiles, (window + Nq - 1 + kKeys - 1) / kKeys + 1 + (std::min(sinks, max_seq_len) + kKeys - 1) / kKeys);
-  // As for the bf16 cache: one wave of items for a batch below the CTA count, otherwise items
-  // of at most kMaxItemTiles tiles from the shared counter (16 sequences of 8k-32k positions
-  // with 32 heads: 450 us at 64 tiles, 434 at 43, 442 at 32); no split under four tiles.
-  constexpr int64_t kMaxItemTiles = 48;
+  // One sequence, or windows (equal lengths): one wave of items.  Sequences of several lengths: items
+  // from the shared counter, about three for each CTA and of at most 48 tiles, so that the longest
+  // sequence does not end alone: 441 us in one wave and 304 in three for 12 sequences of
+  // 30k-60k positions (16 heads), 79 and 61 for 30 of 1k-8k (8 heads), 88 and 90 for 8 of equal
+  // lengths.  Items of under 16 tiles are not made for that, of under four not at all.  (16
+  // sequences of 8k-32k positions with 32 heads: 450 us at 64 tiles, 434 at 43, 442 at 32.)
+  constexpr int64_t kMaxItemTiles = 48, kMinItemTiles = 16, kWaves = 3;
   const int64_t ctas = kCtasPerSm * static_cast<int64_t>(sms);
-  const int64_t s = units < ctas ? ctas / units : (tiles + kMaxItemTiles - 1) / kMaxItemTiles;
+  int64_t s = ctas / units;
+  if (units >= ctas || (B > 1 && !windowed))
+    s = std::max(s, std::min(tiles / kMinItemTiles,
+                             std::max(units < ctas ? kWaves * ctas / units : 1, (tiles + kMaxItemTiles - 1) / kMaxItemTiles)));
   return std::max<int64_t>(1, std::min<int64_t>({s, std::max<int64_t>(1, tiles / 4), kMaxSplits}));
 }
 

@@ -82,6 +82,7 @@ constexpr int kCtasPerSm = 2;
 constexpr int kWg = 128;    // threads of the softmax warpgroup
 constexpr int kKWarp = 4, kVWarp = 5, kPvWarp = 6, kSWarp = 7;
 constexpr int kItemSlots = 4;
+constexpr int kFetchTiles = 2;  // tiles before an item's last at which the next item is fetched
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTop = 9.f;      // weights at the running maximum are 2^kTop
 constexpr float kGrow = 6.f;     // the running maximum moves when a row's grows by more
@@ -257,6 +258,11 @@ __device__ __forceinline__ Item8 take_item8(uint32_t sbase, const uint8_t* smem,
 }
 
 // ------------------------------------------------------------ small pieces
+__device__ __forceinline__ float log2_approx(float x) {  // x normal
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // Barrier of `n` threads that also ors a predicate over them.
 __device__ __forceinline__ bool bar_or(int id, int n, bool pred) {
   uint32_t r;
@@ -315,8 +321,8 @@ __device__ __forceinline__ float unordered(int b) { return __int_as_float(b ^ ((
 
 // ------------------------------------------------------------ loaders
 // One warp for K and one for V, on rings of their own; lane i copies the i-th box of a tile.
-// Page-table entries are read two tiles ahead.  The K warp also fetches the items, one ahead
-// of the one it loads, and publishes them.
+// Page-table entries are read two tiles ahead.  The K warp also fetches the items and
+// publishes them.
 template <int D, int NR>
 __device__ __forceinline__ uint32_t loader8(const Dec8Params& p, uint32_t sbase, uint8_t* smem, const Waiter8& w,
                                             bool kv) {
@@ -332,13 +338,14 @@ __device__ __forceinline__ uint32_t loader8(const Dec8Params& p, uint32_t sbase,
   if (lane == 0) tma_prefetch_map(map);
   const int code = kDRoleLoader << 8;
   uint32_t gt = 0, k_item = 0, slot = 0, round = 0;  // tile gt goes to `slot`, filled `round` times before
-  // A CTA's first item is its own number, the others come from the counter: fetched one ahead
-  // from the start, the CTAs that came first would hold two items each of a single wave.
+  // A CTA's first item is its own number, the others come from the counter, fetched while the
+  // current item's last tiles are asked for: a CTA that holds an item it has not begun leaves
+  // others idle at the end.
   int next = blockIdx.x;
   auto fetch = [&]() {
     if (lane == 0) next = static_cast<int>(gridDim.x + atomicAdd(p.sched, 1u));
   };
-  // Decodes and publishes the fetched item (or the end), and fetches another.
+  // Decodes and publishes the fetched item (or the end).
   auto publish = [&](Item8& it) -> bool {
     const uint32_t s = k_item % kItemSlots;
     if (k_item >= kItemSlots &&
@@ -346,7 +353,6 @@ __device__ __forceinline__ uint32_t loader8(const Dec8Params& p, uint32_t sbase,
       return false;
     const int idx = __shfl_sync(0xffffffffu, next, 0);
     if (idx < p.num_items) {
-      fetch();
       it = item8(p, idx);
     } else {
       it = Item8{};
@@ -361,14 +367,15 @@ __device__ __forceinline__ uint32_t loader8(const Dec8Params& p, uint32_t sbase,
     ++k_item;
     return true;
   };
-  Item8 it, nx;
-  if (!kv && !publish(it)) return 0;
+  Item8 it;
   while (true) {
     if (kv) {
       it = take_item8<L>(sbase, smem, w, k_item, code);
+    } else if (!publish(it)) {
+      break;
     }
     if (it.idx < 0) break;
-    if (!kv && !publish(nx)) break;
+    if (!kv && it.t1 - it.t0 < kFetchTiles) fetch();
     // First position of this lane's box in tile u, or -1 when the box holds nothing the step sees.
     auto box_pos = [&](int u) -> int {
       if (u > it.t1 || lane >= p.loads_per_tile) return -1;
@@ -393,6 +400,7 @@ __device__ __forceinline__ uint32_t loader8(const Dec8Params& p, uint32_t sbase,
       p1 = box_pos(u + 2);
       e1 = entry(p1);
       if (u < it.t0) continue;
+      if (!kv && u == it.t1 - kFetchTiles) fetch();
       if (round > 0 && !w.wait_warp(bar(empty + slot), (round - 1) & 1, code | (empty + slot))) {
         ok = false;
         break;
@@ -409,7 +417,6 @@ __device__ __forceinline__ uint32_t loader8(const Dec8Params& p, uint32_t sbase,
       }
     }
     if (!ok) break;
-    if (!kv) it = nx;
   }
   return gt;
 }
@@ -425,20 +432,20 @@ __device__ __forceinline__ void drain_ring8(uint32_t full, int slots, const DecW
 // One warp: each of the rows b0 .. b1 - 1 of an item becomes two E4M3 terms in shared memory (K-major, in the
 // swizzle of a D-byte row), with its factor 1 / (the row's power of two).
 template <int D, int NR>
-__device__ __noinline__ void prepare_q8(const Dec8Params& p, const Item8& it, uint8_t* smem, uint32_t buf, int b0,
-                                        int b1) {
+__device__ __noinline__ void prepare_q8(const Dec8Params& p, int b, int hkv, int item_row0, int rows, uint8_t* smem,
+                                        uint32_t buf, int b0, int b1) {
   using L = Smem8<D, NR>;
   constexpr int G = D / 16;          // lanes of a row, 16 elements each
   constexpr int kRows = 32 / G;      // rows of a pass
   const int lane = threadIdx.x & 31, c = lane % G;
-  const size_t row0 = (static_cast<size_t>(it.b) * p.Hq + static_cast<size_t>(it.hkv) * p.group) * p.Nq + it.row0;
+  const size_t row0 = (static_cast<size_t>(b) * p.Hq + static_cast<size_t>(hkv) * p.group) * p.Nq + item_row0;
   const uint4* src = reinterpret_cast<const uint4*>(p.q + row0 * D) + 2 * c;
   float* fr = reinterpret_cast<float*>(smem + L::kFrOff) + buf * NR;
   uint8_t* q1 = smem + L::kQOff + buf * L::kQBuf;
 #pragma unroll 1
-  for (int b = b0; b < b1; b += kRows) {
-    const int r = b + lane / G;
-    const bool live = r < it.rows && r < b1;
+  for (int r0 = b0; r0 < b1; r0 += kRows) {
+    const int r = r0 + lane / G;
+    const bool live = r < rows && r < b1;
     const uint4 lo = live ? __ldg(src + static_cast<size_t>(r) * (D / 8)) : make_uint4(0u, 0u, 0u, 0u);
     const uint4 hi = live ? __ldg(src + static_cast<size_t>(r) * (D / 8) + 1) : make_uint4(0u, 0u, 0u, 0u);
     const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -504,7 +511,7 @@ __device__ __forceinline__ void s_role8(const Dec8Params& p, uint32_t sbase, uin
       if (!w.wait_warp(bar(L::kQFull), 0, code | L::kQFull)) break;
       tc_fence_after_sync();
     } else {
-      prepare_q8<D, NR>(p, it, smem, qbuf, 0, NR);
+      prepare_q8<D, NR>(p, it.b, it.hkv, it.row0, it.rows, smem, qbuf, 0, NR);
       if (leader) mbar_arrive(bar(L::kQFull + qbuf));
     }
     const uint64_t qd = q_desc0 + ((qbuf * L::kQBuf) >> 4);
@@ -648,7 +655,7 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
     const uint32_t qbuf = items & 1;
     const float* fr = fr_all + qbuf * NR;
     if (n > 0 && items == 0) {
-      prepare_q8<D, NR>(p, it, smem, 0, warp * (NR / 4), (warp + 1) * (NR / 4));
+      prepare_q8<D, NR>(p, it.b, it.hkv, it.row0, it.rows, smem, 0, warp * (NR / 4), (warp + 1) * (NR / 4));
       bar_or(kBar, kWg, false);
       if (key == 0) mbar_arrive(bar(L::kQFull));
     }
@@ -678,7 +685,7 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       // This tile's scales are used before the next tile's are asked for: the loads share a
       // scoreboard, and a use behind the newer loads waited for those too (850 cycles a tile).
       const float vsc = fminf(fmaxf(vs, kScaleMin), kScaleMax);
-      const float lv = __log2f(vsc), ivs = __frcp_rn(vsc), ksl = ks * p.scale_log2;
+      const float lv = log2_approx(vsc), ivs = dec_exp2(-lv), ksl = ks * p.scale_log2;
       asm volatile("" ::"f"(lv), "f"(ivs), "f"(ksl) : "memory");
       scales_of(it, pos_next, entry_next, ks, vs);
       pos_next = pos_of(it, j + 2);

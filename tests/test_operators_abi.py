@@ -132,13 +132,17 @@ def test_decode_kv8_workspace_bytes(lib):
 def test_decode_kv8_num_splits_without_a_device(lib):
     no_gpu()
     f = lib.attn_decode_kv8_num_splits
-    # 148 SMs of two CTAs assumed: one wave of items for small batches, else items of at most 48
-    # tiles of 128 positions; never fewer than four tiles for a split
+    # 148 SMs of two CTAs assumed: one wave of items for one sequence or windows, else about
+    # three waves of items of 16 to 48 tiles of 128 positions; never under four tiles for a split
     assert f(1, 64, 8, 1, 131072, 1, 0, 0) == 296 // 8
     assert f(32, 32, 32, 1, 131072, 1, 0, 0) == -(-(1024 + 1) // 48)
     assert f(1, 64, 8, 1, 1000, 1, 0, 0) == (8 + 1) // 4
     assert f(1, 32, 8, 1, 131072, 2, 4096, 0) == (32 + 1) // 4
     assert f(1, 32, 8, 1, 131072, 2, 4096, 256) == (32 + 1 + 2) // 4       # the sinks' two tiles
+    assert f(8, 64, 8, 4, 32768, 1, 0, 0) == 3 * 296 // 64
+    assert f(12, 16, 16, 1, 60000, 1, 0, 0) == -(-(469 + 1) // 48)
+    assert f(30, 8, 8, 1, 8192, 1, 0, 0) == 3 * 296 // 240
+    assert f(4, 32, 8, 1, 4096, 1, 0, 0) == (32 + 1) // 4
     assert f(1, 1, 1, 1, 1, 1, 0, 0) == 1
     for bad in ((1, 64, 8, 1, 0, 1, 0, 0), (1, 6, 4, 1, 100, 1, 0, 0), (1, 8, 8, 1, 100, 1, 0, 4),
                 (1, 8, 8, 1, 100, 2, 0, 0), (1, 8, 8, 1, 100, 2, 8, -1), (1, 8, 8, 1, 100, 3, 0, 0)):
