@@ -18,13 +18,15 @@
 // What bounds it: HBM for prefill chunks (every row is read once and written once), the
 // latency of the chain length -> page -> store for a decoding step's few rows.  One CTA
 // takes one unit: the new tokens of one sequence that fall into one aligned run of `unit`
-// slots (a block, or 16 slots), so a block's largest magnitude is found inside one CTA, in
+// slots (a block, or 16 or 32 slots), so a block's largest magnitude is found inside one CTA, in
 // a fixed order, without atomics.  The unit's cos / sin table is computed once into shared
 // memory; a group of D / 16 lanes takes a token's 16-element pieces of one head after another
 // with that token's cosines in registers, four heads' loads in flight.  (Rows dealt to the
 // groups head by head read the table anew for each, four lanes on a bank: 137 us instead of
-// 114 us for 16384 tokens of 64/8 heads.)  The heads are dealt over gridDim.y when there are
-// few units.
+// 112 us for 16384 tokens of 64/8 heads.)  The heads are dealt over gridDim.y when there are
+// few units.  Measured: that chunk at 6000 GB/s, 92 % of a copy's; 8191 tokens of 32/8 heads
+// into E4M3 blocks of 16 in 44.6 us, 63 % (queries alone run at 80 %; a block's codes wait for
+// the maximum of 16 rows, a barrier a head).
 #include "attn.h"
 
 #include <cuda_bf16.h>
@@ -269,16 +271,28 @@ __device__ __forceinline__ void recode16(uint8_t* codes, float ratio) {
   *at = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// MODE 0: bf16 cache; 1, 2, 4: E4M3 cache with units of 16 MODE slots (smaller blocks are runs of a
-// unit of 16), a thread's pieces of a step in registers; 8: larger blocks, read twice.
+// What a CTA's unit is, and how it goes through the heads.  kBf16: 16 slots, no scales.  kSmall,
+// kSmall2: 16 or 32 slots in blocks of up to 16; kBlock2, kBlock4: one block of 32 or 64; their
+// rows stay in registers between the block's maximum and its codes.  kBlock8: one block of 128
+// or 256, read twice.
+enum Mode { kBf16, kSmall, kSmall2, kBlock2, kBlock4, kBlock8 };
+
+// CTAs of an SM.  Most of these kernels' time is latency, so their registers are kept to what lets
+// several CTAs in, as measured: 8191 tokens of 8 heads into blocks of 16 took 31 us at two
+// CTAs, 28 at three, 33 at four (spilling).
+constexpr int ctas_per_sm(int mode) {
+  return mode == kSmall ? 3 : mode == kSmall2 || mode == kBlock2 || mode == kBlock4 ? 2 : 1;
+}
+
 template <int D, int MODE>
-__global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_constant__ AppParams p) {
+__global__ void __launch_bounds__(kAppThreads, ctas_per_sm(MODE))
+    attn_append_kernel(const __grid_constant__ AppParams p) {
   constexpr int G = D / 16;                  // lanes of a row
   constexpr int kRows = kAppThreads / G;     // rows a pass of the CTA takes
   extern __shared__ float2 s_cs[];           // (cos, sin) of the unit's tokens and pairs, see cs_at
   __shared__ Unit s_unit;
   __shared__ float s_amax[2][kAppThreads / 32];
-  __shared__ float s_row[2][2][kRows];       // largest magnitudes of a step's rows, in turn
+  __shared__ float s_row[2][2][kRows];       // largest magnitudes of a head's rows, in turn
   const int tid = threadIdx.x, lane = tid & 31;
   if (tid < 32) {
     const Unit u = find_unit(p, blockIdx.x, lane);
@@ -358,7 +372,7 @@ __global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_c
   if (u.page < 0) return;
   const int h0 = static_cast<int>(static_cast<int64_t>(p.Hkv) * part / parts);
   const int h1 = static_cast<int>(static_cast<int64_t>(p.Hkv) * (part + 1) / parts);
-  if constexpr (MODE == 0) {
+  if constexpr (MODE == kBf16) {
     for (int kv = 0; kv < 2; ++kv) {
       const __nv_bfloat16* base = kv ? p.v : p.k;
       const int64_t stride = kv ? p.v_stride : p.k_stride;
@@ -367,96 +381,111 @@ __global__ void __launch_bounds__(kAppThreads) attn_append_kernel(const __grid_c
       sweep(h0, h1, !kv && turn, [&](int t, int h) { return base + (u.t0 + t) * stride + h * D; },
             [&](int t, int h) { return cache + (static_cast<int64_t>(h) * p.page_size + t) * D; });
     }
-  } else if constexpr (MODE <= 4) {
+  } else if constexpr (MODE != kBlock8) {
     // Half of the CTA takes K and half V; a group of lanes takes slots slot, slot + 16, ... of
-    // the unit, one or two heads a step (with d = 64, every other head).  The largest magnitudes of
-    // a step go to shared memory, and a block's is the largest of its rows': one barrier a step.
-    constexpr int kPass = kRows / 2, kHeads = kPass / 16, kStep = MODE == 1 ? 2 : 1;
+    // the unit, one head after another (with d = 64, every other head), the next head's rows
+    // and scales asked for ahead.  The largest magnitudes of a head's rows go to shared
+    // memory, and a block's is the largest of its rows': one barrier a head.
+    constexpr int kPass = kRows / 2, kHeads = kPass / 16;
+    constexpr int kR = MODE == kSmall ? 1 : MODE == kBlock4 ? 4 : 2;  // rows of a thread
+    constexpr bool kOne = MODE == kBlock2 || MODE == kBlock4;         // ... of one block, or each of its own
+    constexpr int kB = kOne ? 1 : kR;
+    constexpr bool kAhead = MODE != kBlock4;                          // (64 registers more)
     const int kv = g / kPass, slot = g % kPass % 16, hs = g % kPass / 16;
     const __nv_bfloat16* base = (kv ? p.v : p.k);
     const int64_t stride = kv ? p.v_stride : p.k_stride;
     float* scales = kv ? p.v_scale : p.k_scale;
     const int blocks_per_page = p.page_size / p.block;
-    const int b0 = MODE == 1 ? slot / p.block * p.block : 0;  // this thread's block: its first slot,
-    const int first = max(b0, u.slot0);                       // its first new one,
-    const bool has_new = b0 + p.block > u.slot0 && b0 < u.slot0 + u.n;
-    const bool held = has_new && first > b0;                  // and whether it held tokens before
+    const int in16 = kOne ? 0 : slot & ~(p.block - 1);
+    auto b0 = [&](int k) { return 16 * k + in16; };                   // block k of this thread: its first slot,
+    auto first = [&](int k) { return max(b0(k), u.slot0); };          // its first new one,
+    auto has_new = [&](int k) { return b0(k) + p.block > u.slot0 && b0(k) < u.slot0 + u.n; };
+    auto held = [&](int k) { return has_new(k) && u.slot0 > b0(k); }; // and whether it held tokens before
+    auto scale_at = [&](int h, int k) {
+      return scales + (u.page * p.Hkv + h) * blocks_per_page + (u.in_page + b0(k)) / p.block;
+    };
     auto fresh = [&](int r) { return slot + 16 * r >= u.slot0 && slot + 16 * r < u.slot0 + u.n; };
     const bool rotate = !kv && turn;
     float2 cs[8];
-    if (MODE == 1 && rotate && fresh(0)) read_cs(p, s_cs, slot - u.slot0, c, cs);
+    if (kR == 1 && rotate && fresh(0)) read_cs(p, s_cs, slot - u.slot0, c, cs);
     const __nv_bfloat16* src = base + (u.t0 + slot - u.slot0) * stride;
     uint8_t* rows = static_cast<uint8_t*>(kv ? p.v_cache : p.k_cache) +
                     (u.page * p.Hkv * p.page_size + u.in_page + slot) * D;
-    auto values = [&](const uint4& lo, const uint4& hi, int r, float (&a)[8], float (&b)[8]) {
-      widen8(lo, a);
-      widen8(hi, b);
+    struct Rows {
+      uint4 lo[kR], hi[kR];
+      float old[kB];
+    };
+    auto ask = [&](int h, Rows& x) {
+#pragma unroll
+      for (int k = 0; k < kB; ++k) x.old[k] = h < h1 && held(k) ? *scale_at(h, k) : 0.f;
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        if (h < h1 && fresh(r)) {
+          x.lo[r] = __ldg(reinterpret_cast<const uint4*>(src + 16 * r * stride + h * D + at_lo));
+          x.hi[r] = __ldg(reinterpret_cast<const uint4*>(src + 16 * r * stride + h * D + at_hi));
+        }
+      }
+    };
+    auto values = [&](const Rows& x, int r, float (&a)[8], float (&b)[8]) {
+      widen8(x.lo[r], a);
+      widen8(x.hi[r], b);
       if (rotate) {
-        if (MODE > 1) read_cs(p, s_cs, slot + 16 * r - u.slot0, c, cs);
+        if (kR > 1) read_cs(p, s_cs, slot + 16 * r - u.slot0, c, cs);
         rotate16(p.interleaved, cs, a, b);
       }
     };
     int par = 0;
+    Rows x, next;
+    if (kAhead) ask(h0 + hs, next);
 #pragma unroll 1
-    for (int hb = h0 + hs; hb - hs < h1; hb += kStep * kHeads, par ^= 1) {
-      uint4 lo[kStep][MODE], hi[kStep][MODE];
-      float old[kStep];
+    for (int h = h0 + hs; h - hs < h1; h += kHeads, par ^= 1) {
+      if (kAhead) {
+        x = next;
+        ask(h + kHeads, next);
+      } else {
+        ask(h, x);
+      }
+      float amax[kB] = {};
 #pragma unroll
-      for (int q = 0; q < kStep; ++q) {
-        const int h = hb + q * kHeads;
-        old[q] = 0.f;
-        if (held && h < h1)
-          old[q] = scales[(u.page * p.Hkv + h) * blocks_per_page + (u.in_page + b0) / p.block];
-#pragma unroll
-        for (int r = 0; r < MODE; ++r) {
-          if (h < h1 && fresh(r)) {
-            lo[q][r] = __ldg(reinterpret_cast<const uint4*>(src + 16 * r * stride + h * D + at_lo));
-            hi[q][r] = __ldg(reinterpret_cast<const uint4*>(src + 16 * r * stride + h * D + at_hi));
-          }
+      for (int r = 0; r < kR; ++r) {
+        if (h < h1 && fresh(r)) {
+          float a[8], b[8];
+          values(x, r, a, b);
+          amax[r % kB] = fmaxf(amax[r % kB], largest16(a, b));
         }
       }
 #pragma unroll
-      for (int q = 0; q < kStep; ++q) {
-        float amax = 0.f;
+      for (int k = 0; k < kB; ++k) {
 #pragma unroll
-        for (int r = 0; r < MODE; ++r) {
-          if (hb + q * kHeads < h1 && fresh(r)) {
-            float a[8], b[8];
-            values(lo[q][r], hi[q][r], r, a, b);
-            amax = fmaxf(amax, largest16(a, b));
-          }
-        }
-#pragma unroll
-        for (int o = G / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (c == 0) s_row[par][q][g] = amax;
+        for (int o = G / 2; o > 0; o >>= 1) amax[k] = fmaxf(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], o));
+        if (c == 0) s_row[par][k][g] = amax[k];
       }
-      __syncthreads();  // (also: every thread has read the old scales)
+      __syncthreads();  // (also: every thread has read this head's old scales)
 #pragma unroll
-      for (int q = 0; q < kStep; ++q) {
-        const int h = hb + q * kHeads;
-        if (!has_new || h >= h1) continue;
-        float amax = 0.f;
-        const float* rowmax = &s_row[par][q][g - slot + b0];
-        if (MODE > 1 || p.block == 16) {
+      for (int k = 0; k < kB; ++k) {
+        if (!has_new(k) || h >= h1) continue;
+        float top = 0.f;
+        const float* rowmax = &s_row[par][k][g - slot + in16];
+        if (kOne || p.block == 16) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) amax = fmaxf(amax, rowmax[r]);
+          for (int r = 0; r < 16; ++r) top = fmaxf(top, rowmax[r]);
         } else {
-          for (int r = 0; r < p.block; ++r) amax = fmaxf(amax, rowmax[r]);
+          for (int r = 0; r < p.block; ++r) top = fmaxf(top, rowmax[r]);
         }
-        const bool keep = held && old[q] >= 1.17549435e-38f && amax <= 448.f * old[q];
-        const float s = keep ? old[q] : block_scale(amax);
+        const float old = x.old[k];
+        const bool keep = held(k) && old >= 1.17549435e-38f && top <= 448.f * old;
+        const float s = keep ? old : block_scale(top);
         uint8_t* dst = rows + static_cast<int64_t>(h) * p.page_size * D;
 #pragma unroll
-        for (int r = 0; r < MODE; ++r) {
+        for (int r = k; r < kR; r += kB) {
           if (fresh(r)) {
             float a[8], b[8];
-            values(lo[q][r], hi[q][r], r, a, b);
+            values(x, r, a, b);
             encode16(a, b, s, dst + 16 * r * D + at_lo, dst + 16 * r * D + at_hi);
           } else if (!keep && slot + 16 * r < u.slot0) {
-            recode16(dst + 16 * r * D + 16 * c, old[q] / s);
+            recode16(dst + 16 * r * D + 16 * c, old / s);
           }
-          if (!keep && c == 0 && slot + 16 * r == first)
-            scales[(u.page * p.Hkv + h) * blocks_per_page + (u.in_page + b0) / p.block] = s;
+          if (!keep && c == 0 && slot + 16 * r == first(k)) *scale_at(h, k) = s;
         }
       }
     }
@@ -548,11 +577,12 @@ bool allow_smem(int bytes) {
 template <int D>
 cudaError_t launch_append(const AppParams& p, int mode, dim3 grid, size_t smem, cudaStream_t stream) {
   switch (mode) {
-    case 0: attn_append_kernel<D, 0><<<grid, kAppThreads, smem, stream>>>(p); break;
-    case 1: attn_append_kernel<D, 1><<<grid, kAppThreads, smem, stream>>>(p); break;
-    case 2: attn_append_kernel<D, 2><<<grid, kAppThreads, smem, stream>>>(p); break;
-    case 4: attn_append_kernel<D, 4><<<grid, kAppThreads, smem, stream>>>(p); break;
-    default: attn_append_kernel<D, 8><<<grid, kAppThreads, smem, stream>>>(p); break;
+    case kBf16: attn_append_kernel<D, kBf16><<<grid, kAppThreads, smem, stream>>>(p); break;
+    case kSmall: attn_append_kernel<D, kSmall><<<grid, kAppThreads, smem, stream>>>(p); break;
+    case kSmall2: attn_append_kernel<D, kSmall2><<<grid, kAppThreads, smem, stream>>>(p); break;
+    case kBlock2: attn_append_kernel<D, kBlock2><<<grid, kAppThreads, smem, stream>>>(p); break;
+    case kBlock4: attn_append_kernel<D, kBlock4><<<grid, kAppThreads, smem, stream>>>(p); break;
+    default: attn_append_kernel<D, kBlock8><<<grid, kAppThreads, smem, stream>>>(p); break;
   }
   return cudaGetLastError();
 }
@@ -576,7 +606,7 @@ int app_device_setup(AppDevice& out) {
       if (cudaGetSymbolAddress(&addr, g_attn_app_error) != cudaSuccess) return ATTN_ERR_CUDA;
       info.err_word = static_cast<int*>(addr);
       // a unit of 256 slots: 256 x (d/2 + 8) entries of 8 bytes
-      if (!allow_smem<64, 8>(256 * 40 * 8) || !allow_smem<128, 8>(256 * 72 * 8)) return ATTN_ERR_CUDA;
+      if (!allow_smem<64, kBlock8>(256 * 40 * 8) || !allow_smem<128, kBlock8>(256 * 72 * 8)) return ATTN_ERR_CUDA;
     }
     info.probed = true;
   }
@@ -677,8 +707,12 @@ extern "C" int attn_kv_append(const attn_kv_append_args* a, cudaStream_t stream)
   p.num_pages = static_cast<int>(a->num_pages);
   p.max_pages = static_cast<int>(a->max_pages_per_seq);
   p.block = static_cast<int>(fp8 ? a->scale_block : 16);
-  p.unit = std::max(p.block, 16);
   p.per_seq = a->cu_tokens ? 0 : static_cast<int>(a->T / a->B);
+  // Small blocks go two runs of 16 at a time where pages allow it, there are tokens enough for every
+  // SM and no more heads than keep the CTAs short: half the look-ups and cosine tables (8191 tokens
+  // into blocks of 16: 24.7 us instead of 28.0 with 8 heads, 44 and 44 with 16, 79 and 70 with 32).
+  const bool two = fp8 && p.block <= 16 && ps >= 32 && a->Hkv <= 16 && a->T / 32 >= dev.sm_count;
+  p.unit = two ? 32 : std::max(p.block, 16);
   // A run of n positions touches at most (n - 2 + unit) / unit + 1 units.
   int64_t units;
   if (p.per_seq) {
@@ -690,15 +724,20 @@ extern "C" int attn_kv_append(const attn_kv_append_args* a, cudaStream_t stream)
   if (units > lim) return ATTN_ERR_INVALID_ARG;
   // Few units: the heads are dealt evenly over several CTAs of a unit, up to about two CTAs per
   // SM.  (Four per SM: 15.5 us instead of 10.4 for 2048 tokens of 32/8 heads; each CTA computes its
-  // unit's cosines.)  Small blocks of codes are split in two up to four units per SM, whose
-  // second wave would be nearly empty: 49 us instead of 54 for 8191 tokens.
+  // unit's cosines.)  Units of 16 slots of codes are split in two up to four units per SM, whose
+  // second wave would be nearly empty: 68 us instead of 78 for 8191 tokens of 32 KV heads.
   const int64_t want = std::max<int64_t>(fp8 && p.unit == 16 && units < 4 * dev.sm_count ? 2 : 1,
                                          2 * dev.sm_count / units);
   const int64_t part_heads = std::max<int64_t>(1, a->Hkv / want);
   const int64_t parts = std::min<int64_t>((a->Hkv + part_heads - 1) / part_heads, 65535);
   const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>(parts));
   const size_t smem = static_cast<size_t>(p.unit) * (p.half + 8) * sizeof(float2);
-  const int mode = fp8 ? std::min(p.unit / 16, 8) : 0;
+  const int mode = !fp8              ? kBf16
+                   : two             ? kSmall2
+                   : p.unit == 16    ? kSmall
+                   : p.unit == 32    ? kBlock2
+                   : p.unit == 64    ? kBlock4
+                                     : kBlock8;
   return (a->d == 64 ? launch_append<64>(p, mode, grid, smem, stream)
                      : launch_append<128>(p, mode, grid, smem, stream)) == cudaSuccess
              ? ATTN_OK

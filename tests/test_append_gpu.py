@@ -272,3 +272,12 @@ def test_captured_call_follows_the_lengths(cuda_ok):
         assert torch.equal(out, want)
         for a, b in zip(s["caches"] + s["scales"], twin["caches"] + twin["scales"]):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("page,block,d", [(32, 16, 128), (64, 4, 64), (256, 1, 128), (32, 16, 64), (128, 8, 128)])
+def test_long_chunks_of_small_blocks(cuda_ok, page, block, d):
+    """Enough tokens for runs of 32 slots a CTA: ragged starts and ends in either half of a run."""
+    counts, starts = [2000, 1, 17, 0, 2900, 33], [5, 100, 15, 40, 0, 511]
+    for boost in (1.0, 300.0):
+        check(make(6, 3, 1, d, page, block, counts, starts, 21, boost=boost))
+    check(make(6, 2, 2, d, page, block, counts, [s + 16 for s in starts], 22, rot=32), interleaved=True)
