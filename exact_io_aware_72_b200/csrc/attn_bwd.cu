@@ -153,9 +153,11 @@ struct SinkPlan {
 SinkPlan sink_plan(int64_t B, int64_t Hkv, int64_t N, int64_t d, int64_t window, int64_t sinks) {
   SinkPlan s;
   s.sinks = std::min(sinks, N);
-  if (s.sinks < 1 || window >= N - s.sinks) return SinkPlan{};  // every earlier key is visible: plain causal
+  if (s.sinks < 1) return SinkPlan{};
   const int64_t blk = (N + kTile - 1) / kTile;
   s.tiles = (s.sinks + kTile - 1) / kTile;
+  s.parts = 1;
+  if (window >= N - s.sinks) return s;  // every earlier key is visible: no tile stands out
   // A part is about as long as an ordinary key tile's window of query tiles, at least eight
   // tiles (a part's 128 x d fp32 sums take about as long to write as one step).
   const int64_t len = std::max<int64_t>(8, std::min(blk, (window + kTile - 1) / kTile + 1));
@@ -200,7 +202,11 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
   // (and Q, dO) then outgrow L2; there the two-kernel path measured faster.
   const bool fused = (d == 128) && Hq == Hkv && !(opts && opts->bwd_deterministic);
   size_t ws = bwd_workspace_bytes(B, Hq, N, fused ? 128 : 0);
-  const SinkPlan sink = sinks ? sink_plan(B, Hkv, N, d, window, sinks) : SinkPlan{};
+  // A window that covers every earlier key, with the sinks or without, is plain causal attention.
+  // The two-kernel path's sink kernels hold P in more bits than its others (see hold_p), and
+  // keep such a call; the fused kernel holds none.
+  const bool causal = mask_kind == ATTN_MASK_SLIDING_WINDOW && window >= N - sinks && (fused || sinks == 0);
+  const SinkPlan sink = sinks && !causal ? sink_plan(B, Hkv, N, d, window, sinks) : SinkPlan{};
   const size_t part_off = (ws + 255) & ~size_t(255);
   // dK, dV: one key tile per item, or one part of a sink tile's queries.
   const int64_t blk = (N + kTile - 1) / kTile;
@@ -241,8 +247,7 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
       encode_bhnd(enc, &p.tm_do, dout, B * Hq, N, d) != CUDA_SUCCESS)
     return ATTN_ERR_CUDA;
   int kind = mask_kind;
-  int64_t w = window;
-  if (kind == ATTN_MASK_SLIDING_WINDOW && w >= N - sinks) kind = ATTN_MASK_CAUSAL;  // everything earlier is visible
+  if (causal) kind = ATTN_MASK_CAUSAL;
   p.lse = lse;
   p.delta = static_cast<const float*>(workspace);
   p.dq = static_cast<__nv_bfloat16*>(dq);
@@ -255,7 +260,7 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
   p.N = static_cast<int>(N);
   p.group = static_cast<int>(Hq / Hkv);
   p.mask_kind = kind;
-  p.window = static_cast<int>(kind == ATTN_MASK_SLIDING_WINDOW ? w : N);
+  p.window = static_cast<int>(kind == ATTN_MASK_SLIDING_WINDOW ? std::min(window, N) : N);
   p.sinks = static_cast<int>(sink.sinks);  // 0 where the mask is causal
   p.sink_tiles = static_cast<int>(sink.tiles);
   p.sink_parts = static_cast<int>(sink.parts);

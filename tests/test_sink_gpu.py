@@ -215,3 +215,12 @@ def test_training_step_and_generation_agree(cuda_ok):
     assert (glse - lse[:, :, -4:]).abs().max() <= 1e-4
     grads = bwd(q, k, v, out, lse, torch.ones_like(q), mask="sliding_window", window=w, sinks=s)
     assert all(torch.isfinite(g.float()).all() for g in grads)
+
+
+@pytest.mark.parametrize("N,window,sinks", [(1, 1, 1), (7, 6, 1), (300, 299, 1), (513, 10 ** 12, 4), (700, 10, 700), (260, 100, 200),
+                                            (1030, 900, 140)])
+def test_backward_of_covering_windows(cuda_ok, N, window, sinks):
+    """The window and the sinks leave nothing out: causal gradients, from the sinks' own kernels or
+    the fused one."""
+    for heads, d in (((2, 2), 128), ((4, 2), 128), ((3, 1), 64)):
+        backward(1, heads[0], heads[1], N, d, window, sinks, N)
