@@ -77,9 +77,11 @@ struct Unit {
   int first;     // the sequence's first token row
 };
 
-// Which tokens CTA `idx` takes.  Called by one whole warp; n = 0 when there are none.
-__device__ __forceinline__ Unit find_unit(const AppParams& p, int idx, int lane) {
+// Which tokens CTA `idx` takes; n = 0 when there are none.  Called by the whole CTA, every
+// thread of which gets the answer.
+__device__ __forceinline__ Unit find_unit(const AppParams& p, int idx) {
   Unit u{0, 0, 0, 0, 0, -1, 0, 0};
+  const int tid = threadIdx.x;
   int len = 0, n = 0, first = 0, j = 0;
   if (p.per_seq) {
     u.b = idx / p.units_per_seq;
@@ -88,16 +90,19 @@ __device__ __forceinline__ Unit find_unit(const AppParams& p, int idx, int lane)
     first = u.b * n;
     len = __ldg(p.seq_lens + u.b);
     if (len < n || len > p.max_pages * p.page_size) {
-      if (lane == 0) atomicCAS(p.err, 0, kErrSeq | (u.b & 0xFFFFF));
+      if (tid == 0) atomicCAS(p.err, 0, kErrSeq | (u.b & 0xFFFFF));
       return u;
     }
     if (j > (len - 1) / p.unit - (len - n) / p.unit) return u;
   } else {
-    // Units are numbered sequence by sequence: a running count over 32 sequences at a time.
+    // Units are numbered sequence by sequence: a running count, a thread a sequence.  (A warp's
+    // count, 32 sequences at a time, took 82 us for 1024 sequences of one token, this 26.)
+    __shared__ int s_cnt[kAppThreads / 32], s_found[5];
+    const int lane = tid & 31, warp = tid >> 5;
     int before = 0;
     bool found = false;
-    for (int b0 = 0; b0 < p.B && !found; b0 += 32) {
-      const int b = b0 + lane;
+    for (int b0 = 0; b0 < p.B && !found; b0 += kAppThreads) {
+      const int b = b0 + tid;
       int l = 0, c0 = 0, m = 0, cnt = 0;
       if (b < p.B) {
         c0 = __ldg(p.cu_tokens + b);
@@ -116,19 +121,32 @@ __device__ __forceinline__ Unit find_unit(const AppParams& p, int idx, int lane)
         const int x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
       }
-      const unsigned here = __ballot_sync(0xffffffffu, before + incl > idx);
-      if (here) {
-        const int at = __ffs(here) - 1;
-        u.b = b0 + at;
-        len = __shfl_sync(0xffffffffu, l, at);
-        n = __shfl_sync(0xffffffffu, m, at);
-        first = __shfl_sync(0xffffffffu, c0, at);
-        j = idx - before - __shfl_sync(0xffffffffu, incl - cnt, at);
-        found = true;
+      if (lane == 31) s_cnt[warp] = incl;
+      __syncthreads();
+      int total = 0;
+#pragma unroll
+      for (int w = 0; w < kAppThreads / 32; ++w) {
+        if (w == warp) incl += total;
+        total += s_cnt[w];
       }
-      before += __shfl_sync(0xffffffffu, incl, 31);
+      const int at = idx - before - (incl - cnt);  // the unit's number in this sequence
+      if (at >= 0 && at < cnt) {
+        s_found[0] = b;
+        s_found[1] = l;
+        s_found[2] = m;
+        s_found[3] = c0;
+        s_found[4] = at;
+      }
+      __syncthreads();
+      found = idx < before + total;
+      before += total;
     }
     if (!found) return u;
+    u.b = s_found[0];
+    len = s_found[1];
+    n = s_found[2];
+    first = s_found[3];
+    j = s_found[4];
   }
   const int p0 = len - n;                            // position of the sequence's first new token
   const int run = (p0 / p.unit + j) * p.unit;        // first position of the unit
@@ -141,7 +159,7 @@ __device__ __forceinline__ Unit find_unit(const AppParams& p, int idx, int lane)
   const int entry = __ldg(p.block_table + static_cast<int64_t>(u.b) * p.max_pages + run / p.page_size);
   if (entry >= 0 && entry < p.num_pages) {
     u.page = entry;
-  } else if (lane == 0) {
+  } else if (tid == 0) {
     atomicCAS(p.err, 0, kErrPage | (u.b & 0xFFFFF));
   }
   return u;
@@ -290,16 +308,10 @@ __global__ void __launch_bounds__(kAppThreads, ctas_per_sm(MODE))
   constexpr int G = D / 16;                  // lanes of a row
   constexpr int kRows = kAppThreads / G;     // rows a pass of the CTA takes
   extern __shared__ float2 s_cs[];           // (cos, sin) of the unit's tokens and pairs, see cs_at
-  __shared__ Unit s_unit;
   __shared__ float s_amax[2][kAppThreads / 32];
   __shared__ float s_row[2][2][kRows];       // largest magnitudes of a head's rows, in turn
   const int tid = threadIdx.x, lane = tid & 31;
-  if (tid < 32) {
-    const Unit u = find_unit(p, blockIdx.x, lane);
-    if (lane == 0) s_unit = u;
-  }
-  __syncthreads();
-  const Unit u = s_unit;
+  const Unit u = find_unit(p, blockIdx.x);
   if (u.n == 0) return;
   for (int i = tid; i < u.n * p.half; i += kAppThreads) {
     const int t = i / p.half, f = i - t * p.half;

@@ -281,3 +281,25 @@ def test_long_chunks_of_small_blocks(cuda_ok, page, block, d):
     for boost in (1.0, 300.0):
         check(make(6, 3, 1, d, page, block, counts, starts, 21, boost=boost))
     check(make(6, 2, 2, d, page, block, counts, [s + 16 for s in starts], 22, rot=32), interleaved=True)
+
+
+@pytest.mark.parametrize("block", [0, 16])
+def test_batches_wider_than_a_cta(cuda_ok, block):
+    """More sequences than threads of a CTA, some without new tokens, a bad one among them."""
+    import exact_io_aware_72_b200 as attn
+    rs = np.random.RandomState(23)
+    counts, starts = rs.randint(0, 4, 700), rs.randint(0, 40, 700)
+    counts[[255, 256, 511, 512]], counts[600:620] = [1, 3, 0, 2], 0
+    check(make(700, 2, 1, 64, 16, block, counts, starts, 24, tail=5))
+    counts[300] = 2
+    s = make(700, 2, 1, 64, 16, block, counts, starts, 25)
+    whole = [c.clone() for c in s["caches"]]
+    s["seq_lens"][300] = 1                       # fewer positions than new tokens
+    call(s)
+    st, code = attn.kv_append_debug_error()
+    assert st == 1 and code & 0xFFFFF == 300
+    pages = lambda b: [int(s["block_table"][b, i]) for i in range(starts[b] // 16, -(-(starts[b] + counts[b]) // 16))]
+    for c, w in zip(s["caches"], whole):
+        same = (c.view(torch.uint8) == w.view(torch.uint8)).flatten(1).all(1).cpu().numpy()
+        assert same[pages(300)].all()
+        assert not any(same[pages(b)].any() for b in (299, 301, 699, 0) if counts[b])
