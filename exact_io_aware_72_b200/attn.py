@@ -141,6 +141,21 @@ def _check(t: torch.Tensor, name: str, dtype, ndim):
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor with {ndim} dims")
 
 
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on_device(index: int):
+    """Context with device ``index`` current: nothing to enter where it is already (a decoding
+    step's call lasts some 10 us, and a switch and back costs 3 of them)."""
+    return _NO_SWITCH if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+def _stream_handle(stream: Optional[torch.cuda.Stream], index: int) -> int:
+    """``stream``'s handle, or the current stream's of device ``index`` (without the Stream object
+    around it, 5 us)."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
 def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,
         mask: str = "causal", window: Optional[int] = None, out: Optional[torch.Tensor] = None,
         lse: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
@@ -175,11 +190,10 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float
     if out is None:
         out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
     if lse is None:
-        lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, Hq, N), dtype=torch.float32)
     _check(out, "out", out_dtype, 4)
     _check(lse, "lse", torch.float32, 3)
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device)
+    index = q.get_device()
     visits = None
     if item_visits is not None:
         if not (item_visits.is_cuda and item_visits.dtype == torch.int32 and item_visits.is_contiguous()):
@@ -187,29 +201,14 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float
         visits = item_visits.data_ptr()
     opts = FwdOptions(int(wait_timeout_ns), 1 if inject_stall else 0, int(grid_ctas), visits, 1 if p_bf16 else 0,
                       1 if out_fp32 else 0, int(key_offset), 0, int(sinks))
-    with torch.cuda.device(q.device):
+    with _on_device(index):
         st = lib.attn_fwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                              B, Hq, Hkv, N, d, float(scale), MASKS[mask],
-                             int(window) if window is not None else 0, ctypes.c_void_p(stream.cuda_stream),
+                             int(window) if window is not None else 0, _stream_handle(stream, index),
                              ctypes.byref(opts))
     if st != 0:
         raise AttnError(st, "attn_fwd")
     return out, lse
-
-
-_NO_SWITCH = contextlib.nullcontext()
-
-
-def _on_device(index: int):
-    """Context with device ``index`` current: nothing to enter where it is already (a decoding
-    step's call lasts some 10 us, and a switch and back costs 3 of them)."""
-    return _NO_SWITCH if torch.cuda.current_device() == index else torch.cuda.device(index)
-
-
-def _stream_handle(stream: Optional[torch.cuda.Stream], index: int) -> int:
-    """``stream``'s handle, or the current stream's of device ``index`` (without the Stream object
-    around it, 5 us)."""
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _codes(t: torch.Tensor, name: str) -> torch.Tensor:
@@ -240,18 +239,17 @@ def fwd_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: float, k
     if out is None:
         out = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, Hq, N), dtype=torch.float32)
     _check(out, "out", torch.bfloat16, 4)
     _check(lse, "lse", torch.float32, 3)
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device)
+    index = q.get_device()
     opts = FwdOptions(int(wait_timeout_ns), 0, int(grid_ctas))
     opts.sinks = int(sinks)
-    with torch.cuda.device(q.device):
+    with _on_device(index):
         st = lib.attn_fwd_fp8_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), float(q_scale), float(k_scale),
                                  float(v_scale), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, N, d, float(scale),
                                  MASKS[mask], int(window) if window is not None else 0,
-                                 ctypes.c_void_p(stream.cuda_stream), ctypes.byref(opts))
+                                 _stream_handle(stream, index), ctypes.byref(opts))
     if st != 0:
         raise AttnError(st, "attn_fwd_fp8")
     return out, lse
@@ -301,17 +299,16 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ls
         workspace = torch.empty(ws_bytes // 4, dtype=torch.float32, device=q.device)
     if not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device)
+    index = q.get_device()
     opts = FwdOptions(int(wait_timeout_ns), 0, int(grid_ctas))
     opts.bwd_deterministic = int(bool(deterministic))
     opts.sinks = int(sinks)
-    with torch.cuda.device(q.device):
+    with _on_device(index):
         st = lib.attn_bwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                              dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
                              workspace.numel() * workspace.element_size(), B, Hq, Hkv, N, d, float(scale),
                              MASKS[mask], int(window) if window is not None else 0,
-                             ctypes.c_void_p(stream.cuda_stream), ctypes.byref(opts))
+                             _stream_handle(stream, index), ctypes.byref(opts))
     if st != 0:
         raise AttnError(st, "attn_bwd")
     return dq, dk, dv
@@ -383,7 +380,7 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
     _check(out, "out", torch.bfloat16, 4)
     _check(lse, "lse", torch.float32, 3)
     ws_bytes = decode_workspace_bytes(B, Hq, Nq, d, num_splits)
@@ -393,15 +390,14 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     if not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     ws_ptr, ws_len = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device)
+    index = q.get_device()
     opts = FwdOptions(int(wait_timeout_ns), 0, int(grid_ctas), None, 0, 0, 0, 0, int(sinks))
-    with torch.cuda.device(q.device):
+    with _on_device(index):
         st = lib.attn_decode_ex(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                 seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), ws_ptr, ws_len,
                                 B, Hq, Hkv, Nq, d, num_pages, page_size, max_pages, int(num_splits),
                                 float(scale), MASKS[mask], int(window) if window is not None else 0,
-                                ctypes.c_void_p(stream.cuda_stream), ctypes.byref(opts))
+                                _stream_handle(stream, index), ctypes.byref(opts))
     if st != 0:
         raise AttnError(st, "attn_decode")
     return out, lse
