@@ -403,7 +403,7 @@ __device__ __forceinline__ void dq_loader(const BwdParams& p, uint32_t sbase, co
     }
     const int zk = it.b * p.Hkv + it.hkv;
     for (int u = it.lo - it.ns; u <= it.hi; ++u, ++n) {
-      const int j = it.tile(u);
+      const int j = SINK ? it.tile(u) : u;
       const uint32_t slot = n % L::kStages;
       if (n >= (uint32_t)L::kStages &&
           !w.wait(bar(L::kRingEmpty + slot), ((n / L::kStages) - 1) & 1,
@@ -925,7 +925,7 @@ __device__ __forceinline__ void dqf_elem(const BwdParams& p, uint32_t sbase, uin
     const uint64_t c2x2 = f32x2_pack(c2, c2), nlse2x2 = f32x2_pack(nlse, nlse), ndlt2 = f32x2_pack(-dlt, -dlt);
     bool ok = true;
     for (int u = it.lo - it.ns; u <= it.hi && ok; ++u, ++g) {
-      const int j = it.tile(u);
+      const int j = SINK ? it.tile(u) : u;
       if (!w.wait_warp(bar(kSFull), g & 1, code | kSFull)) {
         ok = false;
         break;

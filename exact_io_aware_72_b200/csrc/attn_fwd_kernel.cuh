@@ -107,8 +107,6 @@ struct FwdParams {
   int mask_kind;
   int window;
   int key_offset;    // query row i sits at key position i + key_offset (causal and window masks)
-  int sinks;         // SINK kernels (window mask): keys below it stay visible
-  int sink_tiles;    // ceil(sinks / 128)
   float scale_log2;  // scale * log2(e)
   int pair_heads;    // 1: the two tiles are two heads of one KV group
   int num_mblk;      // ceil(N / 128)
@@ -121,6 +119,8 @@ struct FwdParams {
   float v_scale;     // FP8 inputs: the V tensor's scale, applied to O in the epilogue
   unsigned int* item_visits;  // test hook: per work item, incremented once per visit (or null)
   float* out_f32;    // non-null: out is written here in fp32 (partial results to merge) instead of bf16
+  int sinks;         // SINK kernels (window mask): keys below it stay visible
+  int sink_tiles;    // ceil(sinks / 128)
 };
 
 // EB = bytes per input element: 2 for bf16, 1 for E4M3 (head dim 128 only).
@@ -165,8 +165,14 @@ struct WorkItem {
   int ns;            // SINK kernels: sink tiles before lo_u
   // An item's steps are u = first_u() .. hi_u: the sink tiles 0 .. ns - 1, then tiles lo_u ..
   // hi_u under their own numbers.  Without sinks u is the tile.
-  __device__ __forceinline__ int first_u() const { return lo_u - ns; }
-  __device__ __forceinline__ int tile(int u) const { return u < lo_u ? u - (lo_u - ns) : u; }
+  template <bool SINK>
+  __device__ __forceinline__ int first_u() const {
+    return SINK ? lo_u - ns : lo_u;
+  }
+  template <bool SINK>
+  __device__ __forceinline__ int tile(int u) const {
+    return SINK && u < lo_u ? u - (lo_u - ns) : u;
+  }
 };
 
 // Row r sees keys [r + key_offset - window + 1, r + key_offset] (window), keys
@@ -220,7 +226,7 @@ __device__ __forceinline__ WorkItem decode_item(const FwdParams& p, int hu, int 
       it.hi[t] = 0;
     }
   }
-  it.ns = SINK ? min(p.sink_tiles, it.lo_u) : 0;
+  if constexpr (SINK) it.ns = min(p.sink_tiles, it.lo_u);
   return it;
 }
 
@@ -228,7 +234,8 @@ __device__ __forceinline__ WorkItem decode_item(const FwdParams& p, int hu, int 
 // below hi: key 0 is never behind a row's own position.)
 template <bool SINK>
 __device__ __forceinline__ bool tile_active(const FwdParams& p, int lo, int hi, int j) {
-  return j <= hi && (j >= lo || (SINK && j < p.sink_tiles));
+  if constexpr (SINK) return j <= hi && (j >= lo || j < p.sink_tiles);
+  return j >= lo && j <= hi;
 }
 
 // Does KV tile j need element-wise masking for query block m?
@@ -237,8 +244,11 @@ __device__ __forceinline__ bool tile_is_partial(const FwdParams& p, int m, int j
   const int r0 = m * kBlockM + p.key_offset, c0 = j * kBlockN;
   bool partial = (c0 + kBlockN > p.N);
   if (p.mask_kind != kMaskFull) partial |= (c0 + kBlockN - 1 > r0);
-  if (p.mask_kind == kMaskWindow)
-    partial |= (c0 <= r0 + kBlockM - 1 - p.window) && !(SINK && c0 + kBlockN <= p.sinks);
+  if constexpr (SINK) {
+    partial |= (c0 <= r0 + kBlockM - 1 - p.window) && c0 + kBlockN > p.sinks;
+  } else {
+    if (p.mask_kind == kMaskWindow) partial |= (c0 <= r0 + kBlockM - 1 - p.window);
+  }
   return partial;
 }
 
@@ -392,7 +402,7 @@ __device__ __forceinline__ void vconv_role(const FwdParams& p, uint32_t sbase, c
   int hu, r;
   while (sched.next(hu, r)) {
     const WorkItem it = decode_item<SINK>(p, hu, r);
-    for (int u = it.first_u(); u <= it.hi_u; ++u, ++v) {
+    for (int u = it.first_u<SINK>(); u <= it.hi_u; ++u, ++v) {
       const uint32_t vn = 2 * v + 1, slot = vn % L::kStages;
       const bool got = w.wait(bar(L::kKVFull + slot), (vn / L::kStages) & 1, (kRoleVConv << 8) | (L::kKVFull + slot));
       if (!__all_sync(0xffffffffu, got)) return;
@@ -419,8 +429,8 @@ __device__ __forceinline__ void prefetch_next_item(const FwdParams& p, Schedule 
       if (n.valid[t]) tma_prefetch_3d(&p.tm_q, x, n.mblk[t] * kBlockM, n.b * p.Hq + n.head[t]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      if (n.first_u() + j > n.hi_u) break;
-      const int tile = n.tile(n.first_u() + j);
+      if (n.first_u<SINK>() + j > n.hi_u) break;
+      const int tile = n.tile<SINK>(n.first_u<SINK>() + j);
       tma_prefetch_3d(&p.tm_k, x, tile * kBlockN, n.b * p.Hkv + n.hkv);
       tma_prefetch_3d(&p.tm_v, x, tile * kBlockN, n.b * p.Hkv + n.hkv);
     }
@@ -468,9 +478,9 @@ __device__ __forceinline__ void producer_role(const FwdParams& p, uint32_t sbase
     // A few steps before the item ends, start pulling what the next item
     // reads first (its Q tiles and first K/V tiles) into L2, so the next
     // item's loads do not wait on DRAM.
-    const int pf_step = max(it.first_u(), it.hi_u - kPrefetchSteps);
-    for (int u = it.first_u(); u <= it.hi_u && ok; ++u) {
-      const int j = it.tile(u);
+    const int pf_step = max(it.first_u<SINK>(), it.hi_u - kPrefetchSteps);
+    for (int u = it.first_u<SINK>(); u <= it.hi_u && ok; ++u) {
+      const int j = it.tile<SINK>(u);
       if (u == pf_step) prefetch_next_item<D, EB, SINK>(p, sched);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
@@ -488,7 +498,7 @@ __device__ __forceinline__ void producer_role(const FwdParams& p, uint32_t sbase
           tma_load_3d(sbase + L::kKVOff + slot * L::kTileBytes + c * L::kChunkBytes, map,
                       bar(L::kKVFull + slot), c * L::kChunkElems, j * kBlockN, it.b * p.Hkv + it.hkv, pol_kv);
         ++kv_n;
-        if (u == it.first_u() && kv == 1 && !load_q()) {
+        if (u == it.first_u<SINK>() && kv == 1 && !load_q()) {
           ok = false;
           break;
         }
@@ -620,8 +630,8 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
       return true;
     };
 
-    for (int u = it.first_u(); u <= it.hi_u; ++u) {
-      const int j = it.tile(u);
+    for (int u = it.first_u<SINK>(); u <= it.hi_u; ++u) {
+      const int j = it.tile<SINK>(u);
       const uint32_t kslot = kv_n % L::kStages;
       // K_j is normally resident long before P_t(j-1) is ready; confirming it
       // first lets P V and the next S issue back to back once P arrives.
@@ -634,7 +644,7 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
           ok = false;
           break;
         }
-      } else if (u > it.first_u() && !wait_v_landed(kv_n - 1)) {
+      } else if (u > it.first_u<SINK>() && !wait_v_landed(kv_n - 1)) {
         ok = false;
         break;
       }
@@ -660,7 +670,7 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
       // arrival for a load can only come after the load was issued, i.e.
       // after the slot's previous phase completed: no warp ever arrives twice
       // in one phase, even when its own tile is idle and it runs ahead.
-      if (u > it.first_u()) tc_commit_elect(bar(L::kKVEmpty + (kv_n - 1) % L::kStages));  // V_{j-1} read
+      if (u > it.first_u<SINK>()) tc_commit_elect(bar(L::kKVEmpty + (kv_n - 1) % L::kStages));  // V_{j-1} read
       tc_commit_elect(bar(L::kKVEmpty + kslot));                                   // K_j read
       if (u == it.hi_u) tc_commit_elect(bar(L::kQEmpty));                          // Q read
       if constexpr (kConvV) {
@@ -722,8 +732,8 @@ __device__ __forceinline__ void softmax_role(const FwdParams& p, uint32_t sbase,
     // the turn token back and forth: the exp loop of one tile runs while
     // the tensor core works on the other tile (the exp unit is the shared
     // bottleneck), whether or not a tile has work at a given step.
-    for (int u = it.first_u(); u <= it.hi_u; ++u) {
-      const int j = it.tile(u);
+    for (int u = it.first_u<SINK>(); u <= it.hi_u; ++u) {
+      const int j = it.tile<SINK>(u);
       const bool active = valid && tile_active<SINK>(p, lo, hi, j);
       float s[128];
       if (active) {
