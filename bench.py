@@ -61,9 +61,9 @@ KERNEL_SOURCES = ["exact_io_aware_72_b200/csrc/attn_fwd.cu", "exact_io_aware_72_
 # N = 32768 case (1, 32, 32, 32768, 128) times 4: DRAM bytes grow linearly in N.
 # The FP8 long figure is a capture of the full launch (E4M3 q, k, v: 1.2 GiB).
 NCU_TRAFFIC = {
-    ("dense", "e2664b285cb35e2b"): 410178304 + 111494656,
-    ("long", "e2664b285cb35e2b"): 4 * (937351680 + 253613312),
-    ("long_fp8", "e2664b285cb35e2b"): 2079931136 + 1068808704,
+    ("dense", "e0407f8f6a83f1b5"): 407234048 + 111521024,
+    ("long", "e0407f8f6a83f1b5"): 4 * (895675904 + 252275712),
+    ("long_fp8", "e0407f8f6a83f1b5"): 2078832128 + 1073633792,
 }
 
 
@@ -93,7 +93,7 @@ DECODE_KERNEL_SOURCES = ["exact_io_aware_72_b200/csrc/attn_decode_kernel.cuh", "
 # DRAM bytes per launch of the decoding kernel from one ncu capture, keyed by
 # workload and the hash of the decoding kernel's device sources.
 DECODE_NCU_TRAFFIC = {
-    ("decode_gqa", "786921213997f59a"): 537017856 + 3168000,
+    ("decode_gqa", "a22ec56a6602cd50"): 537001728 + 3086848,
 }
 
 

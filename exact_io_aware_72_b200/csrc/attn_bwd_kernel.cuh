@@ -438,7 +438,8 @@ __device__ __forceinline__ void dq_loader(const BwdParams& p, uint32_t sbase, co
 // after the others (2.2 times the whole time without sinks at N = 16384, window 1024).  So
 // its query tiles are cut into sink_parts items of about a window's length, numbered first;
 // each writes its fp32 sums to the workspace, and attn_bwd_sink_reduce_kernel adds them in a
-// fixed order.
+// fixed order.  (32/8 heads there, 4 sinks: 1355 us, 1100 without sinks; dQ 497 -> 535, dK and dV
+// 582 -> 739: a tenth more work, a wave of items more, and P's longer form, see hold_p.)
 struct DkvItem {
   int b, hkv, n, qlo, qhi, steps;  // steps = group * (qhi - qlo + 1)
   int part;                        // SINK kernels: index of the item's partial sums, -1 if none

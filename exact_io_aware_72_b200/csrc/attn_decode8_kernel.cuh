@@ -52,6 +52,13 @@
 // decoded once (by the K loader) and read from shared memory.  With everything inlined the
 // kernel was 130 KB, and each item's start and end ran at the speed of instruction fetches,
 // 10 us an item.
+//
+// Measured, with the bytes of the visible codes and scales over 6544 GB/s (a copy) as 100 %: one
+// sequence of 131072 positions, 64/8 heads, 51.5 us (79 %: the start and the end of the one wave
+// of items, 12 us, are not overlapped); 16 of 8k-32k with 32 heads 416 us (99 %); 32 windows of 4096 with
+// 4 sinks 52 us (79 %); 8 of 16k-32k with 32 rows (four new tokens, groups of 8) 114 us (54 %: the
+// softmax warps' 3300 cycles a tile, two tiles at a time on an SM, against the 1400 in
+// which HBM delivers one).
 #pragma once
 
 #include <cuda.h>

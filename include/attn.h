@@ -1,6 +1,7 @@
 /*
  * Exact attention forward (bf16 and FP8, on device or host buffers), backward, paged-KV
- * decoding and the partial-result merge of ring attention for NVIDIA B200 (sm_100a): C ABI.
+ * decoding over bf16 and 8-bit caches, the cache's append and the partial-result merge of ring
+ * attention for NVIDIA B200 (sm_100a): C ABI.
  *
  * Computes, for every batch b, query head h and query row i,
  *
