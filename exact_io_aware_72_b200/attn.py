@@ -376,7 +376,9 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     if max_seq_len is None:
         max_seq_len = max_pages * page_size
     if num_splits is None:
-        num_splits = decode_num_splits(B, Hq, Hkv, Nq, max_seq_len, mask, window)
+        # (the count goes by the tiles that are read: the window's and the sinks')
+        seen = window if window is None or not sinks else window + min(int(sinks), int(max_seq_len))
+        num_splits = decode_num_splits(B, Hq, Hkv, Nq, max_seq_len, mask, seen)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:

@@ -2,6 +2,9 @@
 refused before anything is launched, host-only sizes, the binding's checks, and the fp64
 references against plainer forms of the same mathematics."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -77,6 +80,22 @@ def test_append_valid_arguments_reach_the_device_check(lib):
     assert call_append(lib, T=0, k=None, v=None, q=None, q_out=None, cu_tokens=None) == 4
     # K and V as views of one projection's rows; the last row ends where the buffer does
     assert call_append(lib, k_stride=1536, v_stride=1536, q_stride=1536, k=Q + 2048, v=Q + 2560) == 4
+
+
+@pytest.mark.parametrize("name,struct", [("attn_fwd_options", A.FwdOptions), ("attn_kv_append_args", A.KvAppendArgs)])
+def test_binding_structs_match_the_header(name, struct, tmp_path):
+    """Every field of the ctypes structs lies where a C compiler puts the header's."""
+    cc, cuda = shutil.which("gcc"), os.path.join(os.path.dirname(os.path.dirname(BLD.nvcc_path())), "include")
+    if cc is None or not os.path.exists(os.path.join(cuda, "cuda_runtime.h")):
+        pytest.skip("no C compiler or CUDA headers")
+    lines = "".join(f'printf("%zu\\n", offsetof({name}, {f[0]}));' for f in struct._fields_)
+    (tmp_path / "o.c").write_text('#include <stddef.h>\n#include <stdio.h>\n#include "attn.h"\nint main(void) {' + lines +
+                                  f'printf("%zu\\n", sizeof({name})); return 0; }}')
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([cc, "-I" + os.path.join(root, "include"), "-I" + cuda, "-o", str(tmp_path / "o"),
+                    str(tmp_path / "o.c")], check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "o")], capture_output=True, text=True).stdout.split()]
+    assert got == [getattr(struct, f[0]).offset for f in struct._fields_] + [ctypes.sizeof(struct)]
 
 
 # ------------------------------------------------------------------ 8-bit decoding
