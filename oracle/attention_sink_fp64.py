@@ -46,7 +46,8 @@ def forward(q, k, v, scale, window, sinks, key_offset=0):
 def backward(q, k, v, dout, scale, window, sinks):
     """((dq, dk, dv), bounds) of sum(dout * out).  The bounds count the roundings of a backward
     that holds P and dS in bf16 (8 significant bits: spacing 2^-7 of the leading bit, so a
-    rounding is off by up to 2^-8 of the value; dS carries P's and its own), takes D from a bf16
+    rounding is off by up to 2^-8 of the value; dS carries P's and its own; P on its way to dv may
+    be rounded to fp16 first, 2^-11 more), takes D from a bf16
     out (2^-8 of each |dout out|) and forms scores in fp32 (d + 8 roundings of the sum of |q k|): elementwise
     limits before the results' own rounding."""
     q, k, v, dout = (np.asarray(t, np.float64) for t in (q, k, v, dout))
@@ -71,7 +72,7 @@ def backward(q, k, v, dout, scale, window, sinks):
             e_ds = np.abs(ds) * (2.0 ** -7 + slip) + p * (off + (dp_mass + np.abs(D)) * d * 2.0 ** -24)
             lim[0][b, h] = scale * e_ds @ np.abs(kk)
             lim[1][b, h // g] += scale * e_ds.T @ np.abs(qq)
-            lim[2][b, h // g] += (p * (2.0 ** -8 + slip)).T @ np.abs(do)
+            lim[2][b, h // g] += (p * (2.0 ** -8 + 2.0 ** -11 + slip)).T @ np.abs(do)
     return got, lim
 
 
