@@ -147,7 +147,7 @@ _NO_SWITCH = contextlib.nullcontext()
 def _on_device(index: int):
     """Context with device ``index`` current: nothing to enter where it is already (a decoding
     step's call lasts some 10 us, and a switch and back costs 3 of them)."""
-    return _NO_SWITCH if torch.cuda.current_device() == index else torch.cuda.device(index)
+    return _NO_SWITCH if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
 
 
 def _stream_handle(stream: Optional[torch.cuda.Stream], index: int) -> int:
@@ -211,11 +211,15 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float
     return out, lse
 
 
-def _codes(t: torch.Tensor, name: str) -> torch.Tensor:
-    if isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn:
-        t = t.view(torch.uint8)
-    _check(t, name, torch.uint8, 4)
-    return t
+def _codes(t: torch.Tensor, name: str):
+    """E4M3 codes, as bytes or as the type itself (only their address and shape are used)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _CODE_TYPES or t.dim() != 4 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of E4M3 codes (uint8 or float8_e4m3fn) with 4 dims")
+
+
+_CODE_TYPES = (torch.float8_e4m3fn, torch.uint8)
 
 
 def fwd_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: float, k_scale: float, v_scale: float,
@@ -227,7 +231,9 @@ def fwd_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: float, k
     torch.float8_e4m3fn, [B,H,N,128]) whose values are code * q_scale (k_scale,
     v_scale); returns (out bf16 [B,Hq,N,128], lse fp32 [B,Hq,N]).  ``sinks`` as in ``fwd``."""
     lib = load_library()
-    q, k, v = _codes(q, "q"), _codes(k, "k"), _codes(v, "v")
+    _codes(q, "q")
+    _codes(k, "k")
+    _codes(v, "v")
     B, Hq, N, d = q.shape
     Bk, Hkv, Nk, dk = k.shape
     if (Bk, Nk, dk) != (B, N, d) or tuple(v.shape) != tuple(k.shape):
@@ -487,7 +493,8 @@ def decode_kv8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
     """
     lib = load_library()
     _check(q, "q", torch.bfloat16, 4)
-    k_cache, v_cache = _codes(k_cache, "k_cache"), _codes(v_cache, "v_cache")
+    _codes(k_cache, "k_cache")
+    _codes(v_cache, "v_cache")
     _check(k_scale, "k_scale", torch.float32, 3)
     _check(v_scale, "v_scale", torch.float32, 3)
     _check(block_table, "block_table", torch.int32, 2)
@@ -524,14 +531,14 @@ def decode_kv8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
     for t in (k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse, workspace):
         if t.get_device() != index:
             raise ValueError("all tensors must be on one device")
-    opts = FwdOptions(int(wait_timeout_ns), 0, int(grid_ctas))
+    opts = ctypes.byref(FwdOptions(int(wait_timeout_ns), 0, int(grid_ctas))) if wait_timeout_ns or grid_ctas else None
     with _on_device(index):
         st = lib.attn_decode_kv8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                                  v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
                                  lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, B, Hq, Hkv, Nq, d,
                                  num_pages, page_size, max_pages, page_size // per_page, int(num_splits),
                                  float(scale), MASKS[mask], int(window) if window is not None else 0, int(sinks),
-                                 _stream_handle(stream, index), ctypes.byref(opts))
+                                 _stream_handle(stream, index), opts)
     if st != 0:
         raise AttnError(st, "attn_decode_kv8")
     return out, lse
@@ -562,6 +569,10 @@ def _rows(t: torch.Tensor, name: str, T, H, d):
     return s0 if shape[0] > 1 else max(s0, shape[1] * shape[2])
 
 
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
               block_table: torch.Tensor, seq_lens: torch.Tensor, q: Optional[torch.Tensor] = None,
               cu_tokens: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
@@ -587,7 +598,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     v_stride = _rows(v, "v", T, Hkv, d)
     fp8 = k_scale is not None or v_scale is not None
     if fp8:
-        k_cache, v_cache = _codes(k_cache, "k_cache"), _codes(v_cache, "v_cache")
+        _codes(k_cache, "k_cache")
+        _codes(v_cache, "v_cache")
         _check(k_scale, "k_scale", torch.float32, 3)
         _check(v_scale, "v_scale", torch.float32, 3)
     else:
@@ -606,19 +618,13 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
                 or page_size % per_page:
             raise ValueError("k_scale and v_scale must be [num_pages, Hkv, page_size / block]")
         block = page_size // per_page
-    a = KvAppendArgs(k=k.data_ptr(), v=v.data_ptr(), k_stride=k_stride, v_stride=v_stride,
-                     k_cache=k_cache.data_ptr(), v_cache=v_cache.data_ptr(), block_table=block_table.data_ptr(),
-                     seq_lens=seq_lens.data_ptr(), B=B, T=T, Hkv=Hkv, d=d, num_pages=num_pages, page_size=page_size,
-                     max_pages_per_seq=max_pages, scale_block=block, interleaved=1 if interleaved else 0)
     given = [v, k_cache, v_cache, block_table, seq_lens]
     if fp8:
-        a.k_scale, a.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
         given += [k_scale, v_scale]
     for t, name, dtype in ((cu_tokens, "cu_tokens", torch.int32), (positions, "positions", torch.int32),
                            (inv_freq, "inv_freq", torch.float32)):
         if t is not None:
             _check(t, name, dtype, 1)
-            setattr(a, name, t.data_ptr())
             given.append(t)
     if cu_tokens is not None and cu_tokens.shape[0] != B + 1:
         raise ValueError("cu_tokens must have B + 1 entries")
@@ -626,26 +632,28 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         raise ValueError("without cu_tokens the number of tokens must be a multiple of the number of sequences")
     if positions is not None and positions.shape[0] != T:
         raise ValueError("positions must have one entry for each token")
-    if inv_freq is not None:
-        a.rot_dim = 2 * inv_freq.shape[0]
+    q_stride = Hq = 0
     if q is not None:
-        a.q_stride = _rows(q, "q", T, None, d)
-        a.q, a.Hq = q.data_ptr(), q.shape[1]
+        q_stride, Hq = _rows(q, "q", T, None, d), q.shape[1]
         given.append(q)
-        shape = (T, q.shape[1], d) if cu_tokens is not None else (B, q.shape[1], T // B, d)
+        shape = (T, Hq, d) if cu_tokens is not None else (B, Hq, T // B, d)
         if q_out is None:
             q_out = q.new_empty(shape)
         _check(q_out, "q_out", torch.bfloat16, len(shape))
         if tuple(q_out.shape) != shape:
             raise ValueError("q_out has the wrong shape")
         given.append(q_out)
-        a.q_out = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     index = k.get_device()
     for t in given:
         if t.get_device() != index:
             raise ValueError("all tensors must be on one device")
+    a = KvAppendArgs(_ptr(q), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride, _ptr(q_out), k_cache.data_ptr(),
+                     v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), block_table.data_ptr(), seq_lens.data_ptr(),
+                     _ptr(cu_tokens), _ptr(positions), _ptr(inv_freq), B, T, Hq, Hkv, d,
+                     0 if inv_freq is None else 2 * inv_freq.shape[0], num_pages, page_size, max_pages, block,
+                     1 if interleaved else 0)
     with _on_device(index):
         st = lib.attn_kv_append(ctypes.byref(a), _stream_handle(stream, index))
     if st != 0:
