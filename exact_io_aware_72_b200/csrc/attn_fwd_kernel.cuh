@@ -245,7 +245,7 @@ __device__ __forceinline__ bool tile_is_partial(const FwdParams& p, int m, int j
   bool partial = (c0 + kBlockN > p.N);
   if (p.mask_kind != kMaskFull) partial |= (c0 + kBlockN - 1 > r0);
   if constexpr (SINK) {
-    partial |= (c0 <= r0 + kBlockM - 1 - p.window) && c0 + kBlockN > p.sinks;
+    if (p.mask_kind == kMaskWindow) partial |= (c0 <= r0 + kBlockM - 1 - p.window) && !(c0 + kBlockN <= p.sinks);
   } else {
     if (p.mask_kind == kMaskWindow) partial |= (c0 <= r0 + kBlockM - 1 - p.window);
   }
