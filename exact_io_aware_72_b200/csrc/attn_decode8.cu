@@ -296,7 +296,10 @@ extern "C" int attn_decode_kv8(const void* q, const void* k_cache, const void* v
     mp.num_splits = static_cast<int>(num_splits);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(rows));
-    cfg.blockDim = dim3(128);
+    // Eight warps where there are splits for them and room beside the other rows: 49.3 us instead of
+    // 50.6 for 64 rows of 37 splits, 119 instead of 117 for 2048 rows of 20.
+    const bool wide = num_splits > 16 && rows <= 4 * dev.sm_count;
+    cfg.blockDim = dim3(wide ? 256 : 128);
     cfg.dynamicSmemBytes = static_cast<size_t>(num_splits) * sizeof(float);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
@@ -304,8 +307,10 @@ extern "C" int attn_decode_kv8(const void* q, const void* k_cache, const void* v
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = d == 64 ? cudaLaunchKernelEx(&cfg, attn_decode8_merge_kernel<64>, mp)
-                                  : cudaLaunchKernelEx(&cfg, attn_decode8_merge_kernel<128>, mp);
+    const cudaError_t e = d == 64 ? (wide ? cudaLaunchKernelEx(&cfg, attn_decode8_merge_kernel<64, 8>, mp)
+                                          : cudaLaunchKernelEx(&cfg, attn_decode8_merge_kernel<64, 4>, mp))
+                                  : (wide ? cudaLaunchKernelEx(&cfg, attn_decode8_merge_kernel<128, 8>, mp)
+                                          : cudaLaunchKernelEx(&cfg, attn_decode8_merge_kernel<128, 4>, mp));
     if (e != cudaSuccess) return ATTN_ERR_CUDA;
   }
   return ATTN_OK;

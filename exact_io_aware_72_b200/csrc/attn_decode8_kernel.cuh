@@ -54,8 +54,8 @@
 // 10 us an item.
 //
 // Measured, with the bytes of the visible codes and scales over 6544 GB/s (a copy) as 100 %: one
-// sequence of 131072 positions, 64/8 heads, 51.5 us (79 %: the start and the end of the one wave
-// of items, 12 us, are not overlapped); 16 of 8k-32k with 32 heads 416 us (99 %); 32 windows of 4096 with
+// sequence of 131072 positions, 64/8 heads, 49.4 us (83 %: the start and the end of the one wave
+// of items, the merge and the launches, 8 us, are not overlapped); 16 of 8k-32k with 32 heads 416 us (99 %); 32 windows of 4096 with
 // 4 sinks 52 us (79 %); 8 of 16k-32k with 32 rows (four new tokens, groups of 8) 114 us (54 %: the
 // softmax warps' 3300 cycles a tile, two tiles at a time on an SM, against the 1400 in
 // which HBM delivers one).
@@ -1008,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode8_kernel(cons
 
 // ------------------------------------------------------------ split merge
 // One CTA per query row: out = sum_s w_s O_s / sum_s w_s, w_s = 2^(lse2_s - max lse2), lse = ln
-// sum_s 2^lse2_s.  Warp g takes splits g, g + 4, ..., a lane D / 32 columns; its first loads of O
+// sum_s 2^lse2_s.  Warp g of W takes splits g, g + W, ..., a lane D / 32 columns; its first loads of O
 // are under way while the weights are formed.  Sums in a fixed order.
 struct Merge8Params {
   const float* part_o;
@@ -1019,11 +1019,11 @@ struct Merge8Params {
 };
 constexpr int kMergeBatch = 8;  // splits of a warp whose loads are in flight together
 
-template <int D>
-__global__ void __launch_bounds__(128) attn_decode8_merge_kernel(const Merge8Params p) {
+template <int D, int W>
+__global__ void __launch_bounds__(32 * W) attn_decode8_merge_kernel(const Merge8Params p) {
   constexpr int V = D / 32;
   extern __shared__ float s_w[];  // [num_splits]
-  __shared__ float s_red[2][4], s_acc[3][D];
+  __shared__ float s_red[2][W], s_acc[W - 1][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int S = p.num_splits;
@@ -1032,7 +1032,7 @@ __global__ void __launch_bounds__(128) attn_decode8_merge_kernel(const Merge8Par
   auto load = [&](int first) {
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const int k = first + 4 * u;
+      const int k = first + W * u;
 #pragma unroll
       for (int v = 0; v < V; ++v) o[u][v] = 0.f;
       if (k < S) {
@@ -1053,7 +1053,7 @@ __global__ void __launch_bounds__(128) attn_decode8_merge_kernel(const Merge8Par
   };
   load(warp);
   float top = -INFINITY;
-  for (int k = tid; k < S; k += 128) {
+  for (int k = tid; k < S; k += 32 * W) {
     const float l2 = __ldcg(p.part_lse + static_cast<size_t>(row) * S + k);
     s_w[k] = l2;
     top = fmaxf(top, l2);
@@ -1062,7 +1062,8 @@ __global__ void __launch_bounds__(128) attn_decode8_merge_kernel(const Merge8Par
   for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
   if (lane == 0) s_red[0][warp] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3]));
+#pragma unroll
+  for (int g = 0; g < W; ++g) top = fmaxf(top, s_red[0][g]);
   const float base = top == -INFINITY ? 0.f : top;
   float acc[V], wsum = 0.f;
 #pragma unroll
@@ -1070,13 +1071,13 @@ __global__ void __launch_bounds__(128) attn_decode8_merge_kernel(const Merge8Par
   for (int k0 = warp;; ) {
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const int k = k0 + 4 * u;
+      const int k = k0 + W * u;
       const float w = k < S ? attn_sm100_dec::dec_exp2(s_w[k] - base) : 0.f;
       wsum += w;
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] = fmaf(w, o[u][v], acc[v]);
     }
-    k0 += 4 * kMergeBatch;
+    k0 += W * kMergeBatch;
     if (k0 >= S) break;
     load(k0);
   }
@@ -1087,14 +1088,19 @@ __global__ void __launch_bounds__(128) attn_decode8_merge_kernel(const Merge8Par
   }
   __syncthreads();
   if (warp > 0) return;
-  wsum = (s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]);
+  wsum = 0.f;
+#pragma unroll
+  for (int g = 0; g < W; ++g) wsum += s_red[1][g];
+#pragma unroll
+  for (int g = 0; g < W - 1; ++g) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] += s_acc[g][lane * V + v];
+  }
   const float inv = wsum != 0.f ? 1.f / wsum : 0.f;
   __nv_bfloat16* dst = p.out + static_cast<size_t>(row) * D + lane * V;
 #pragma unroll
   for (int v = 0; v < V; v += 2) {
-    const int c = lane * V + v;
-    const float a = ((acc[v] + s_acc[0][c]) + (s_acc[1][c] + s_acc[2][c])) * inv;
-    const float b = ((acc[v + 1] + s_acc[0][c + 1]) + (s_acc[1][c + 1] + s_acc[2][c + 1])) * inv;
+    const float a = acc[v] * inv, b = acc[v + 1] * inv;
     *reinterpret_cast<uint32_t*>(dst + v) = attn_sm100_dec::dec_pack_bf16x2(a, b);
   }
   if (lane == 0) p.lse[row] = wsum != 0.f ? (top + __log2f(wsum)) * kLn2 : -INFINITY;
