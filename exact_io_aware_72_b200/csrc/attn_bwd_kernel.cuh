@@ -825,7 +825,7 @@ __device__ __forceinline__ void dkv_elem(const BwdParams& p, uint32_t sbase, uin
 //   dQ += dS(g-1) K  once dS(g-1) is in Y,
 //   dP(g) -> Y       behind it,
 // so the exponentials of tile g run while the tensor core does dQ of tile g-1
-// and dP of tile g.  P is kept as bf16 until dP arrives.
+// and dP of tile g.  P is kept as bf16 (sinks: fp16, see hold_p) until dP arrives.
 template <int D, bool SINK>
 __device__ __forceinline__ void dqf_mma(const BwdParams& p, uint32_t sbase, uint32_t tmem, const BwdWaiter& w) {
   using L = BwdSmem<D>;
@@ -1013,8 +1013,8 @@ __device__ __forceinline__ void dqf_elem(const BwdParams& p, uint32_t sbase, uin
 //   dV, dK (g-1)     once P^T(g-1) and dS^T(g-1) are in Y,
 //   dP^T(g) -> Y     behind them (in issue order, so after they read Y),
 // so the exponentials of step g run while the tensor core does dV, dK of step g-1
-// and dP^T of step g.  P is kept as bf16 until dP arrives; dS = P (dP - D) is
-// formed from that bf16 P.
+// and dP^T of step g.  P is kept as bf16 (sinks: fp16, see hold_p) until dP arrives; dS =
+// P (dP - D) is formed from that P.
 template <int D, bool SINK>
 __device__ __forceinline__ void dkvf_mma(const BwdParams& p, uint32_t sbase, uint32_t tmem, const BwdWaiter& w) {
   using L = BwdSmem<D>;

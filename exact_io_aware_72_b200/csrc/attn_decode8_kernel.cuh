@@ -941,7 +941,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode8_kernel(cons
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + L::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
   volatile uint32_t* loaded = reinterpret_cast<volatile uint32_t*>(smem + L::kMiscOff + 8);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be set up; it waits for this grid's end
+  // The merge may be set up; it waits for this grid's end.  (Without splits the next kernel is not
+  // this library's: it might take tensor memory before this CTA has.)
+  if (p.num_splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
     for (int i = 0; i < 2; ++i) {
