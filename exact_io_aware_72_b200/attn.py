@@ -156,6 +156,25 @@ def _stream_handle(stream: Optional[torch.cuda.Stream], index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
+def _on_stream(stream: Optional[torch.cuda.Stream]):
+    """Context in which a call allocates (and fills) what its caller did not bring: ``stream`` current,
+    so that a block's earlier use, its fill, the kernels and its next use follow one another there.
+    Blocks of the current stream would be taken while that stream's earlier work still uses them,
+    filled without an order, and handed on while ``stream`` still runs."""
+    return _NO_SWITCH if stream is None else torch.cuda.stream(stream)
+
+
+def _output(like: torch.Tensor, shape, dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A new output of a call on ``stream``.  Its block, once the caller drops it, also waits for what the
+    caller's current stream has been given by then."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
 def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,
         mask: str = "causal", window: Optional[int] = None, out: Optional[torch.Tensor] = None,
         lse: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
@@ -166,7 +185,8 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float
 
     q: [B,Hq,N,d], k/v: [B,Hkv,N,d], bf16, contiguous, on one CUDA device.
     ``mask`` is "full", "causal" or "sliding_window" (keys i-window < j <= i).
-    The launch is asynchronous on ``stream`` (default: the current stream).
+    The launch is asynchronous on ``stream`` (default: the current stream), to which, here and in
+    the other calls, belongs what the call allocates: workspaces, and outputs not given.
     ``p_bf16`` selects bf16 P for V values beyond the fp16 range (see
     include/attn.h); ``item_visits`` (int32 CUDA tensor of num_work_items
     counters) is a test hook counting each work item's visits; ``out_fp32``
@@ -188,9 +208,9 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float
         scale = 1.0 / math.sqrt(d)
     out_dtype = torch.float32 if out_fp32 else torch.bfloat16
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        out = _output(q, q.shape, out_dtype, stream)
     if lse is None:
-        lse = q.new_empty((B, Hq, N), dtype=torch.float32)
+        lse = _output(q, (B, Hq, N), torch.float32, stream)
     _check(out, "out", out_dtype, 4)
     _check(lse, "lse", torch.float32, 3)
     index = q.get_device()
@@ -243,9 +263,9 @@ def fwd_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: float, k
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
+        out = _output(q, (B, Hq, N, d), torch.bfloat16, stream)
     if lse is None:
-        lse = q.new_empty((B, Hq, N), dtype=torch.float32)
+        lse = _output(q, (B, Hq, N), torch.float32, stream)
     _check(out, "out", torch.bfloat16, 4)
     _check(lse, "lse", torch.float32, 3)
     index = q.get_device()
@@ -290,9 +310,9 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ls
         raise ValueError(f"mask must be one of {sorted(MASKS)}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _output(q, q.shape, q.dtype, stream) if dq is None else dq
+    dk = _output(k, k.shape, k.dtype, stream) if dk is None else dk
+    dv = _output(v, v.shape, v.dtype, stream) if dv is None else dv
     for t, name, ref in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
         _check(t, name, torch.bfloat16, 4)
         if t.shape != ref.shape:
@@ -302,7 +322,8 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ls
     if sinks and mask == "sliding_window" and window is not None:
         ws_bytes = int(lib.attn_bwd_sink_workspace_bytes(B, Hq, Hkv, N, d, int(window), int(sinks)))
     if workspace is None:
-        workspace = torch.empty(ws_bytes // 4, dtype=torch.float32, device=q.device)
+        with _on_stream(stream):
+            workspace = torch.empty(ws_bytes // 4, dtype=torch.float32, device=q.device)
     if not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     index = q.get_device()
@@ -386,15 +407,16 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
         seen = window if window is None or not sinks else window + min(int(sinks), int(max_seq_len))
         num_splits = decode_num_splits(B, Hq, Hkv, Nq, max_seq_len, mask, seen)
     if out is None:
-        out = torch.empty_like(q)
+        out = _output(q, q.shape, q.dtype, stream)
     if lse is None:
-        lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
+        lse = _output(q, (B, Hq, Nq), torch.float32, stream)
     _check(out, "out", torch.bfloat16, 4)
     _check(lse, "lse", torch.float32, 3)
     ws_bytes = decode_workspace_bytes(B, Hq, Nq, d, num_splits)
     if workspace is None:
         # zero-filled: its first 256 bytes are the work counter, which each call leaves at zero
-        workspace = torch.zeros(ws_bytes // 4, dtype=torch.float32, device=q.device)
+        with _on_stream(stream):
+            workspace = torch.zeros(ws_bytes // 4, dtype=torch.float32, device=q.device)
     if not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     ws_ptr, ws_len = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -516,15 +538,16 @@ def decode_kv8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
         num_splits = decode_kv8_num_splits(B, Hq, Hkv, Nq, max_pages * page_size if max_seq_len is None else max_seq_len,
                                            mask, window, sinks)
     if out is None:
-        out = torch.empty_like(q)
+        out = _output(q, q.shape, q.dtype, stream)
     if lse is None:
-        lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
+        lse = _output(q, (B, Hq, Nq), torch.float32, stream)
     _check(out, "out", torch.bfloat16, 4)
     _check(lse, "lse", torch.float32, 3)
     if out.shape != q.shape or tuple(lse.shape) != (B, Hq, Nq):
         raise ValueError("out or lse has the wrong shape")
     if workspace is None:
-        workspace = decode_kv8_workspace(B, Hq, Hkv, Nq, d, num_splits, q.device)
+        with _on_stream(stream):
+            workspace = decode_kv8_workspace(B, Hq, Hkv, Nq, d, num_splits, q.device)
     if not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     index = q.get_device()
@@ -638,7 +661,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         given.append(q)
         shape = (T, Hq, d) if cu_tokens is not None else (B, Hq, T // B, d)
         if q_out is None:
-            q_out = q.new_empty(shape)
+            q_out = _output(q, shape, q.dtype, stream)
         _check(q_out, "q_out", torch.bfloat16, len(shape))
         if tuple(q_out.shape) != shape:
             raise ValueError("q_out has the wrong shape")
@@ -755,10 +778,11 @@ def _fwd_host(fp8: bool, q, k, v, q_scale, k_scale, v_scale, scale, mask, window
         raise ValueError("out and lse must be contiguous host tensors: bf16 [B,Hq,N,d] and fp32 [B,Hq,N]")
     device = torch.device(device)
     if staging is None:
-        staging = (torch.empty(q.shape, dtype=dt, device=device), torch.empty(k.shape, dtype=dt, device=device),
-                   torch.empty(k.shape, dtype=dt, device=device),
-                   torch.empty(out.shape, dtype=torch.bfloat16, device=device),
-                   torch.empty(lse.shape, dtype=torch.float32, device=device))
+        with _on_stream(stream):
+            staging = (torch.empty(q.shape, dtype=dt, device=device), torch.empty(k.shape, dtype=dt, device=device),
+                       torch.empty(k.shape, dtype=dt, device=device),
+                       torch.empty(out.shape, dtype=torch.bfloat16, device=device),
+                       torch.empty(lse.shape, dtype=torch.float32, device=device))
     sq, sk, sv, so, sl = staging
     for t, ref, name in ((sq, q, "q"), (sk, k, "k"), (sv, v, "v"), (so, out, "out"), (sl, lse, "lse")):
         if not t.is_cuda or t.dtype != ref.dtype or tuple(t.shape) != tuple(ref.shape) or not t.is_contiguous():
