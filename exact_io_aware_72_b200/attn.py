@@ -613,7 +613,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     rows; without it every sequence has T / B.  ``inv_freq`` (fp32 [rot / 2]) turns the
     rotation on, by the cache's positions or ``positions`` (int32 [T]).  With ``q``
     [T, Hq, d] its rotated rows are returned: [B, Hq, T / B, d] as ``decode`` takes them, or
-    [T, Hq, d] with ``cu_tokens``.  One launch on ``stream`` (default: the current stream).
+    [T, Hq, d] with ``cu_tokens``.  Without ``cu_tokens`` seq_lens[b] = 0 marks an idle slot, as in
+    ``decode_kv8``: nothing of it is read or cached, its queries are zeros.  One launch on ``stream`` (default: the current stream).
     """
     lib = load_library()
     k_stride = _rows(k, "k", None, None, None)

@@ -69,7 +69,7 @@ struct AppParams {
 
 struct Unit {
   int b;
-  int t0, n;     // first token row of the unit, number of new tokens in it
+  int t0, n;     // first token row of the unit, number of new tokens in it (-1 - j: unit j of an idle slot)
   int slot0;     // slot of the first new token inside the unit
   int pos0;      // position of the first new token
   int64_t page;  // physical page, -1 if unusable
@@ -89,6 +89,10 @@ __device__ __forceinline__ Unit find_unit(const AppParams& p, int idx) {
     n = p.per_seq;
     first = u.b * n;
     len = __ldg(p.seq_lens + u.b);
+    if (len == 0) {
+      u.n = -1 - j;
+      return u;
+    }
     if (len < n || len > p.max_pages * p.page_size) {
       if (tid == 0) atomicCAS(p.err, 0, kErrSeq | (u.b & 0xFFFFF));
       return u;
@@ -302,6 +306,17 @@ constexpr int ctas_per_sm(int mode) {
   return mode == kSmall ? 3 : mode == kSmall2 || mode == kBlock2 || mode == kBlock4 ? 2 : 1;
 }
 
+// An idle slot's queries are zeros, its CTAs sharing the rows: the decoding step does not read them,
+// but what the caller is handed is defined.
+template <int D>
+__device__ __noinline__ void zero_queries(const AppParams& p, int b, int unit) {
+  const int64_t pieces = static_cast<int64_t>(p.Hq) * p.per_seq * (D / 8);
+  uint4* dst = reinterpret_cast<uint4*>(p.q_out) + b * pieces;
+  const int64_t cta = static_cast<int64_t>(unit) * gridDim.y + blockIdx.y;
+  const int64_t ctas = static_cast<int64_t>(p.units_per_seq) * gridDim.y;
+  for (int64_t i = cta * kAppThreads + threadIdx.x; i < pieces; i += ctas * kAppThreads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 template <int D, int MODE>
 __global__ void __launch_bounds__(kAppThreads, ctas_per_sm(MODE))
     attn_append_kernel(const __grid_constant__ AppParams p) {
@@ -312,7 +327,10 @@ __global__ void __launch_bounds__(kAppThreads, ctas_per_sm(MODE))
   __shared__ float s_row[2][2][kRows];       // largest magnitudes of a head's rows, in turn
   const int tid = threadIdx.x, lane = tid & 31;
   const Unit u = find_unit(p, blockIdx.x);
-  if (u.n == 0) return;
+  if (u.n <= 0) {
+    if (u.n < 0 && p.q) zero_queries<D>(p, u.b, -1 - u.n);
+    return;
+  }
   for (int i = tid; i < u.n * p.half; i += kAppThreads) {
     const int t = i / p.half, f = i - t * p.half;
     const int pos = p.positions ? __ldg(p.positions + u.t0 + t) : u.pos0 + t;

@@ -464,12 +464,16 @@ int attn_decode_static(const void* q, const void* k_cache, const void* v_cache, 
  *   k_cache, v_cache  device, bf16 or E4M3 codes, [num_pages, Hkv, page_size, d], 16-byte aligned
  *   k_scale, v_scale  device, fp32, as above; NULL exactly where scale_block is 0
  *   block_table   device, int32, [B, max_pages_per_seq]
- *   seq_lens      device, int32, [B]; n_b <= seq_lens[b] <= max_pages_per_seq * page_size
+ *   seq_lens      device, int32, [B]; n_b <= seq_lens[b] <= max_pages_per_seq * page_size, or 0 (idle)
  *   cu_tokens     device, int32, [B + 1], or NULL (T % B == 0)
  *   positions     device, int32, [T]: the rotation's positions; NULL: the cache's positions
  *   inv_freq      device, fp32, [rot_dim / 2]; NULL exactly where rot_dim is 0 (no rotation)
  *   rot_dim       0 .. d, a multiple of 16;  d in {64, 128};  page_size in {16, 32, 64, 128, 256}
  *   scale_block   0 (bf16 cache) or a power of two <= page_size
+ *
+ * Without cu_tokens seq_lens[b] == 0 marks an idle slot of a padded batch, as in attn_decode_kv8: its
+ * rows of q, k and v and its table are not read, nothing is cached, its rows of q_out are zeros,
+ * no error. (With cu_tokens an idle slot has no rows.)
  *
  * A sequence whose length or row range is unusable is skipped, as are the cache rows of a page
  * entry outside [0, num_pages); both are reported by attn_kv_append_debug_error as
