@@ -22,10 +22,13 @@
 //   scalars, and no thread computes an exponential that no row needs.
 // * O^T = V^T P^T (d x NR): A is the V tile read MN-major, B is P written to shared memory by
 //   the softmax threads, 16 rows (16 bytes) per key.  E4M3 V needs an 8-bit P: the weight is
-//   held as a sum of three E5M2 numbers (3 significant bits each, 9 together: off by at most
-//   2^-9, half of a bf16 weight's rounding), three products into one accumulator.  Weights are
-//   scaled so that m sits at 2^9: they reach 2^15 before m must move (E5M2 ends at 57344),
-//   and a weight is lost only below 2^-26 of the largest.
+//   rounded to fp16 and held as a sum of three E5M2 numbers (3 significant bits each, 9
+//   together: off by at most 2^-9 + 2^-11, a bf16 weight by 2^-8), three products into one
+//   accumulator.  Weights are scaled so that m sits at 2^12: they reach 2^15 before m must move
+//   (E5M2 ends at 57344), and E5M2's smallest step, 2^-16, rounds them to 2^-28 of the largest: nine
+//   bits are kept down to about 2^-20 of it, none below 2^-29.  (With m at 2^9 and room for a
+//   growth of 2^6 a long context's many small weights beside one large were lost from 2^-26 on.)
+//   What is held is softmax weight times V scale, so "the largest" is the largest of these.
 // * Sums l and all statistics are fp32; out is rounded once to bf16.
 //
 // Work items and splits are the bf16 decoding kernel's.  Two CTAs share an
@@ -34,7 +37,7 @@
 // runs under the other's tiles.  (One CTA whose two warpgroups took the tiles of an item in
 // turn stopped for it: 9 us for each item, 70 us instead of 58 for a batch of windows.)
 // m is per row: a vote over the warpgroup (one hardware barrier with a reduction) finds the
-// rare tiles where some row's maximum grew by more than 2^6.
+// rare tiles where some row's maximum grew by more than 2^3 (32 rows: 115 us, 114 with room for 2^6).
 //
 // The partial results of splits are merged by a second, small kernel whose launch overlaps the
 // first one's end (programmatic dependent launch).  Merged by the CTA that finished last, they
@@ -91,8 +94,8 @@ constexpr int kKWarp = 4, kVWarp = 5, kPvWarp = 6, kSWarp = 7;
 constexpr int kItemSlots = 4;
 constexpr int kFetchTiles = 2;  // tiles before an item's last at which the next item is fetched
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kTop = 9.f;      // weights at the running maximum are 2^kTop
-constexpr float kGrow = 6.f;     // the running maximum moves when a row's grows by more
+constexpr float kTop = 12.f;     // weights at the running maximum are 2^kTop
+constexpr float kGrow = 3.f;     // the running maximum moves when a row's grows by more
 constexpr float kNoMax = -3e38f; // running maximum of a row that has seen no key
 constexpr float kScaleMin = 9.094947017729282e-13f, kScaleMax = 1099511627776.f;  // 2^-40, 2^40
 
@@ -750,8 +753,9 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
       // The last product has read P, and O may be changed.
       if (gi > 0) failed |= !w.wait(bar(L::kPVDone), (gi - 1) & 1, code | L::kPVDone);
       if (grown) {
-        // Every warp's row maxima, then m and factor of every row: a row's m moves to its
-        // maximum when that is more than kGrow above it.
+        // Every warp's row maxima, then m and factor of every row: m moves to the maximum of each
+        // row that grew at all (moving only those that grew by more than kGrow, the others did it in
+        // later tiles: 120 us instead of 115 for 8 x 16k-32k positions and 32 rows).
         tc_fence_after_sync();
 #pragma unroll
         for (int ch = 0; ch < CH; ++ch) {
@@ -773,7 +777,7 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
         if (key < NR) {
           const float mx = fmaxf(fmaxf(wmax[key], wmax[NR + key]), fmaxf(wmax[2 * NR + key], wmax[3 * NR + key]));
           const float old = negm[key];
-          const bool move = mx + old > kTop + kGrow && mx < INFINITY;
+          const bool move = mx + old > kTop && mx < INFINITY;
           const float now = move ? kTop - mx : old;
           negm_all[(mbuf ^ 1) * NR + key] = now;
           coef[key] = move ? dec_exp2(now - old) : 1.f;

@@ -530,8 +530,9 @@ int attn_kv_append_debug_error(cudaStream_t stream, int* device_code);
  *
  * Precision: the products take the codes exactly; a bf16 query row is split into two E4M3
  * terms (exact to 2^-18 of the row's largest element); scores, statistics and sums are fp32;
- * softmax weights go to the product with V as sums of three E5M2 numbers (9 significant bits,
- * one more than bf16's); weights below 2^-26 of a row's largest are dropped there (and only there).
+ * the weights that the product with V takes, w = softmax weight * V scale, are sums of three
+ * E5M2 numbers: off by at most (2^-9 + 2^-11) w + 2^-29 M, with M the row's largest w (bf16's
+ * rounding is 2^-8 w; a w below 2^-29 M is lost there, and only there: the weights' sum has it).
  * Ownership, checks, overlap rules, bounded waits and errors as attn_decode.
  */
 int attn_decode_kv8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
