@@ -16,8 +16,8 @@
 // * S^T = K Q^T (128 keys x NR query rows, NR = 16 or 32): an SS product with the K
 //   tile as A and Q as B.  bf16 q has 8 significant bits and E4M3 holds 4, so each q row,
 //   scaled by a power of two to a maximum in [128, 256), is the sum of two E4M3 numbers:
-//   the rounded value and the rest, which fits 4 bits exactly (elements below 2^-10 of the
-//   row's largest keep an absolute error of 2^-18 of it).  Both terms accumulate into S.
+//   the rounded value and the rest, which fits 4 bits exactly (elements below 2^-9 of the
+//   row's largest keep an absolute error of up to 2^-17 of it).  Both terms accumulate into S.
 // * A softmax thread owns one key (TMEM lane) and its NR scores, so its scales and mask are
 //   scalars, and no thread computes an exponential that no row needs.
 // * O^T = V^T P^T (d x NR): A is the V tile read MN-major, B is P written to shared memory by

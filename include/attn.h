@@ -529,7 +529,7 @@ int attn_kv_append_debug_error(cudaStream_t stream, int* device_code);
  *   opts              wait bound and CTA count as for attn_fwd_ex; may be NULL
  *
  * Precision: the products take the codes exactly; a bf16 query row is split into two E4M3
- * terms (exact to 2^-18 of the row's largest element); scores, statistics and sums are fp32;
+ * terms (exact to 2^-17 of the row's largest element); scores, statistics and sums are fp32;
  * the weights that the product with V takes, w = softmax weight * V scale, are sums of three
  * E5M2 numbers: off by at most (2^-9 + 2^-11) w + 2^-29 M, with M the row's largest w (bf16's
  * rounding is 2^-8 w; a w below 2^-29 M is lost there, and only there: the weights' sum has it).

@@ -1,6 +1,10 @@
 """The 8-bit terms of the decoding step's products, modelled on the host number for number: what the
 header says of their rounding."""
+import os
+import re
+
 import numpy as np
+import torch
 
 
 def e5m2_terms(w):
@@ -26,3 +30,15 @@ def test_weights_keep_nine_bits_above_a_step():
             assert (err <= w * (2.0 ** -9 + 2.0 ** -11)).all()
     # the largest weight and its terms are E5M2 numbers
     assert max(t.max() for t in e5m2_terms(np.float32([2.0 ** 15]))) <= 57344
+
+
+def test_queries_are_two_e4m3_numbers():
+    """Every bf16 element of a row whose largest has been scaled into [128, 256)."""
+    x = torch.arange(1 << 15, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).float()
+    x = x[x < 256]
+    first = x.to(torch.float8_e4m3fn).float()
+    rest = (x - first - (x - first).to(torch.float8_e4m3fn).float()).abs().double()
+    assert not rest[x >= 0.25].any()                      # 2^-9 of 128: exact from there on
+    assert float(rest.max()) / 128 == 2.0 ** -17          # what the header gives, and no more
+    header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "attn.h")
+    assert re.search(r"two E4M3\s+\*?\s*terms \(exact to 2\^-17 of the row's largest element\)", open(header).read())
