@@ -164,13 +164,13 @@ def _on_stream(stream: Optional[torch.cuda.Stream]):
     return _NO_SWITCH if stream is None else torch.cuda.stream(stream)
 
 
-def _output(like: torch.Tensor, shape, dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """A new output of a call on ``stream``.  Its block, once the caller drops it, also waits for what the
-    caller's current stream has been given by then."""
+def _output(like: torch.Tensor, stream: Optional[torch.cuda.Stream], shape=None, dtype=None) -> torch.Tensor:
+    """A new output of a call on ``stream``, by default like ``like``.  Its block, once the caller drops
+    it, also waits for what the caller's current stream has been given by then."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty_like(like, dtype=dtype) if shape is None else like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        t = like.new_empty(shape, dtype=dtype)
+        t = torch.empty_like(like, dtype=dtype) if shape is None else like.new_empty(shape, dtype=dtype)
     t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
@@ -208,9 +208,9 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float
         scale = 1.0 / math.sqrt(d)
     out_dtype = torch.float32 if out_fp32 else torch.bfloat16
     if out is None:
-        out = _output(q, q.shape, out_dtype, stream)
+        out = _output(q, stream, dtype=out_dtype)
     if lse is None:
-        lse = _output(q, (B, Hq, N), torch.float32, stream)
+        lse = _output(q, stream, (B, Hq, N), torch.float32)
     _check(out, "out", out_dtype, 4)
     _check(lse, "lse", torch.float32, 3)
     index = q.get_device()
@@ -263,9 +263,9 @@ def fwd_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: float, k
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = _output(q, (B, Hq, N, d), torch.bfloat16, stream)
+        out = _output(q, stream, dtype=torch.bfloat16)
     if lse is None:
-        lse = _output(q, (B, Hq, N), torch.float32, stream)
+        lse = _output(q, stream, (B, Hq, N), torch.float32)
     _check(out, "out", torch.bfloat16, 4)
     _check(lse, "lse", torch.float32, 3)
     index = q.get_device()
@@ -310,9 +310,9 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ls
         raise ValueError(f"mask must be one of {sorted(MASKS)}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dq = _output(q, q.shape, q.dtype, stream) if dq is None else dq
-    dk = _output(k, k.shape, k.dtype, stream) if dk is None else dk
-    dv = _output(v, v.shape, v.dtype, stream) if dv is None else dv
+    dq = _output(q, stream) if dq is None else dq
+    dk = _output(k, stream) if dk is None else dk
+    dv = _output(v, stream) if dv is None else dv
     for t, name, ref in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)):
         _check(t, name, torch.bfloat16, 4)
         if t.shape != ref.shape:
@@ -407,9 +407,9 @@ def decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
         seen = window if window is None or not sinks else window + min(int(sinks), int(max_seq_len))
         num_splits = decode_num_splits(B, Hq, Hkv, Nq, max_seq_len, mask, seen)
     if out is None:
-        out = _output(q, q.shape, q.dtype, stream)
+        out = _output(q, stream)
     if lse is None:
-        lse = _output(q, (B, Hq, Nq), torch.float32, stream)
+        lse = _output(q, stream, (B, Hq, Nq), torch.float32)
     _check(out, "out", torch.bfloat16, 4)
     _check(lse, "lse", torch.float32, 3)
     ws_bytes = decode_workspace_bytes(B, Hq, Nq, d, num_splits)
@@ -538,9 +538,9 @@ def decode_kv8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
         num_splits = decode_kv8_num_splits(B, Hq, Hkv, Nq, max_pages * page_size if max_seq_len is None else max_seq_len,
                                            mask, window, sinks)
     if out is None:
-        out = _output(q, q.shape, q.dtype, stream)
+        out = _output(q, stream)
     if lse is None:
-        lse = _output(q, (B, Hq, Nq), torch.float32, stream)
+        lse = _output(q, stream, (B, Hq, Nq), torch.float32)
     _check(out, "out", torch.bfloat16, 4)
     _check(lse, "lse", torch.float32, 3)
     if out.shape != q.shape or tuple(lse.shape) != (B, Hq, Nq):
@@ -662,7 +662,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         given.append(q)
         shape = (T, Hq, d) if cu_tokens is not None else (B, Hq, T // B, d)
         if q_out is None:
-            q_out = _output(q, shape, q.dtype, stream)
+            q_out = _output(q, stream, shape)
         _check(q_out, "q_out", torch.bfloat16, len(shape))
         if tuple(q_out.shape) != shape:
             raise ValueError("q_out has the wrong shape")
