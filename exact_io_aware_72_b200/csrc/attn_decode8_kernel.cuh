@@ -205,13 +205,14 @@ __device__ __forceinline__ Item8 item8(const Dec8Params& p, int idx) {
   it.b = idx / p.Hkv;
   it.L = __ldg(p.seq_lens + it.b);
   it.bad = (it.L != 0 && it.L < p.Nq) || it.L > p.max_pages * p.page_size;
+  if (it.bad) it.L = 0;  // nothing of it is looked up
   it.row0 = rc * p.rows_chunk;
   it.rows = min(p.rows_chunk, p.rows_total - it.row0);
   it.lo_pos = it.ns = it.first = it.t0 = 0;
   it.sinks = 0;
   it.t1 = -1;
   it.pad[0] = it.pad[1] = 0;
-  if (!it.bad && it.L > 0) {
+  if (it.L > 0) {
     if (p.mask_kind == kDMaskWindow) {
       it.lo_pos = max(0, it.L - p.Nq - p.window + 1);
       it.sinks = min(p.sinks, it.L);
@@ -317,6 +318,15 @@ __device__ __forceinline__ uint64_t desc8(uint32_t saddr, uint32_t lbo, uint32_t
 __host__ __device__ constexpr uint32_t idesc8(int N, uint32_t a_fmt, uint32_t b_fmt, bool a_mn, bool b_mn) {
   return (1u << 4) | (a_fmt << 7) | (b_fmt << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(kKeys >> 4) << 24);
+}
+// *at, or 0 without a read.  (As a branch it cost the 32-row kernel 100 bytes of spills.)
+__device__ __forceinline__ int load_if(bool read, const int* at) {
+  int v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
+      : "=&r"(v)
+      : "l"(at), "r"(read ? 1u : 0u));
+  return v;
 }
 __device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -630,21 +640,23 @@ __device__ __forceinline__ void softmax_role8(const Dec8Params& p, uint32_t sbas
 
   // What the threads of an item ask for ahead: the scales of this thread's key, loaded a tile
   // ahead, and their page-table entry two tiles ahead.  Where there is no such tile, or the
-  // step does not see the key, position 0 stands in: its weight is zero whatever is read.
+  // step does not see the key, the sequence's last position, which it always sees, stands in (the
+  // weight is zero whatever is read): other pages may be another's by now.  Without a length (an
+  // idle slot, no more items) that is -1, and nothing is read.
   const int hkv_block = p.page_shift - p.block_shift;
   auto pos_of = [&](const Item8& it, int j) -> int {
     const int pos = it.tile(it.t0 + j) * kKeys + key;
-    return it.t0 + j <= it.t1 && it.seen(pos) ? pos : 0;
+    return it.t0 + j <= it.t1 && it.seen(pos) ? pos : it.L - 1;
   };
   auto entry_of = [&](const Item8& it, int pos) -> int {
-    return __ldg(p.block_table + static_cast<size_t>(it.b) * p.max_pages + (pos >> p.page_shift));
+    return load_if(pos >= 0, p.block_table + static_cast<size_t>(it.b) * p.max_pages + (pos >> p.page_shift));
   };
   auto scales_of = [&](const Item8& it, int pos, int entry, float& ks, float& vs) {
     const int page = static_cast<unsigned>(entry) < static_cast<unsigned>(p.num_pages) ? entry : 0;
     const size_t at = (static_cast<size_t>(page * p.Hkv + it.hkv) << hkv_block) +
                       ((pos & (p.page_size - 1)) >> p.block_shift);
-    ks = __ldg(p.k_scale + at);
-    vs = __ldg(p.v_scale + at);
+    ks = __int_as_float(load_if(pos >= 0, reinterpret_cast<const int*>(p.k_scale + at)));
+    vs = __int_as_float(load_if(pos >= 0, reinterpret_cast<const int*>(p.v_scale + at)));
   };
 
   Item8 it = take_item8<L>(sbase, smem, w, k_item, code);
