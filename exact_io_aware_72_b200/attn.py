@@ -294,8 +294,10 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ls
     workspace (allocated here when not given) holds the row terms
     D = rowsum(dout * out) and, on the fused path (d = 128, Hq == Hkv), the fp32
     sums of dq: ``attn_bwd_workspace_bytes(B, Hq, N)`` bytes there, B*Hq*N floats
-    otherwise, and ``attn_bwd_sink_workspace_bytes`` with ``sinks``.  ``deterministic`` takes the two-kernel path there too (dq bitwise
-    reproducible; seven matmuls per pair instead of five).
+    otherwise, and behind them, with ``sinks``, the partial sums of the key tiles that
+    hold sinks (``attn_bwd_sink_workspace_bytes``).  ``deterministic`` takes the
+    two-kernel path there too (dq bitwise reproducible; seven matmuls per pair
+    instead of five).
     """
     lib = load_library()
     for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out"), (dout, "dout")):
@@ -320,7 +322,9 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ls
     fused = d == 128 and Hq == Hkv and not deterministic  # the library's choice of path
     ws_bytes = int(lib.attn_bwd_workspace_bytes(B, Hq, N)) if fused else 4 * B * Hq * N
     if sinks and mask == "sliding_window" and window is not None:
-        ws_bytes = int(lib.attn_bwd_sink_workspace_bytes(B, Hq, Hkv, N, d, int(window), int(sinks)))
+        # the sink tiles' partial sums lie behind what this path takes without them
+        parts = (int(lib.attn_bwd_sink_workspace_bytes(B, Hq, Hkv, N, d, int(window), n)) for n in (int(sinks), 0))
+        ws_bytes = (ws_bytes + 255) // 256 * 256 + max(0, next(parts) - next(parts))
     if workspace is None:
         with _on_stream(stream):
             workspace = torch.empty(ws_bytes // 4, dtype=torch.float32, device=q.device)

@@ -176,7 +176,7 @@ size_t attn_bwd_workspace_bytes(int64_t B, int64_t Hq, int64_t N) {
 size_t attn_bwd_sink_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t d, int64_t window,
                                      int64_t sinks) {
   if (!sizes_ok(B, Hq, Hkv, N) || (d != 64 && d != 128) || window < 1 || sinks < 0) return 0;
-  const size_t base = bwd_workspace_bytes(B, Hq, N, 128);
+  const size_t base = bwd_workspace_bytes(B, Hq, N, Hq == Hkv ? 128 : 0);  // shared heads: no dQ sums
   const SinkPlan s = sink_plan(B, Hkv, N, d, window, sinks);
   if (base == 0 || s.bytes > (size_t(1) << 61)) return 0;
   return ((base + 255) & ~size_t(255)) + s.bytes;

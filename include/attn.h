@@ -298,9 +298,11 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* out, co
 size_t attn_bwd_workspace_bytes(int64_t B, int64_t Hq, int64_t N);
 
 /* Workspace bytes attn_bwd_ex needs with the sliding window and sinks > 0, 16-byte aligned (0 for
-   invalid sizes): attn_bwd_workspace_bytes and room for the fp32 partial sums of the key tiles
-   that hold sinks, whose queries are cut into parts. A workspace too small for the path taken is
-   refused. dk and dv stay bitwise reproducible: the parts are added in a fixed order. */
+   invalid sizes): attn_bwd_workspace_bytes (with Hq != Hkv 4 B Hq N bytes, all that those calls
+   take) and room for the fp32 partial sums of the key tiles that hold sinks, whose queries are cut
+   into parts. That room, the difference to the size with sinks = 0, lies behind what the call takes
+   without sinks, rounded up to 256 bytes: 4 B Hq N bytes also with d = 64 or bwd_deterministic. A
+   workspace too small for the path taken is refused. dk and dv stay bitwise reproducible: the parts are added in a fixed order. */
 size_t attn_bwd_sink_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t N, int64_t d, int64_t window,
                                      int64_t sinks);
 
