@@ -510,12 +510,14 @@ def decode_kv8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
                window: Optional[int] = None, sinks: int = 0, num_splits: Optional[int] = None,
                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
-               wait_timeout_ns: int = 0, grid_ctas: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
+               wait_timeout_ns: int = 0, grid_ctas: int = 0, inject_stall: int = 0
+               ) -> Tuple[torch.Tensor, torch.Tensor]:
     """``decode`` over an 8-bit paged cache: k_cache/v_cache hold E4M3 codes (uint8 or
     float8_e4m3fn, [num_pages,Hkv,page_size,d]) with one fp32 scale for each block of tokens
     and head (k_scale/v_scale [num_pages,Hkv,page_size/block], as ``kv_append`` writes them).
     With the sliding window, ``sinks`` first positions stay visible.  seq_lens[b] = 0 marks an
-    idle slot (out 0, lse -inf).  Returns (out bf16 [B,Hq,Nq,d], lse fp32 [B,Hq,Nq]).
+    idle slot (out 0, lse -inf).  ``inject_stall`` (a test hook) stops a CTA's loads before its
+    n-th tile.  Returns (out bf16 [B,Hq,Nq,d], lse fp32 [B,Hq,Nq]).
     """
     lib = load_library()
     _check(q, "q", torch.bfloat16, 4)
@@ -558,7 +560,9 @@ def decode_kv8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
     for t in (k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, lse, workspace):
         if t.get_device() != index:
             raise ValueError("all tensors must be on one device")
-    opts = ctypes.byref(FwdOptions(int(wait_timeout_ns), 0, int(grid_ctas))) if wait_timeout_ns or grid_ctas else None
+    opts = None
+    if wait_timeout_ns or grid_ctas or inject_stall:
+        opts = ctypes.byref(FwdOptions(int(wait_timeout_ns), int(inject_stall), int(grid_ctas)))
     with _on_device(index):
         st = lib.attn_decode_kv8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                                  v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),

@@ -282,6 +282,7 @@ extern "C" int attn_decode_kv8(const void* q, const void* k_cache, const void* v
   p.num_items = static_cast<int>(items);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = (opts && opts->wait_timeout_ns) ? opts->wait_timeout_ns : kDefaultTimeoutNs;
+  p.stall = (opts && opts->inject_stall > 0) ? static_cast<unsigned>(opts->inject_stall) - 1u : 0xffffffffu;
 
   int grid = static_cast<int>(std::min<int64_t>(items, kCtasPerSm * dev.sm_count));
   if (opts && opts->grid_ctas > 0) grid = std::min(grid, opts->grid_ctas);

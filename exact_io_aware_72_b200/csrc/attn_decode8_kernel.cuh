@@ -120,6 +120,7 @@ struct Dec8Params {
   int num_splits, num_items;
   float scale_log2;
   unsigned long long timeout_ns;
+  unsigned int stall;      // test hook: loads before a CTA's loaders stop (0xffffffff: they do not)
   unsigned int* sched;     // [0] next work item, [1] CTAs finished; zero between launches
 };
 
@@ -420,6 +421,10 @@ __device__ __forceinline__ uint32_t loader8(const Dec8Params& p, uint32_t sbase,
       p1 = box_pos(u + 2);
       e1 = entry(p1);
       if (u < it.t0) continue;
+      if (gt == p.stall) {
+        ok = false;
+        break;
+      }
       if (!kv && u == it.t1 - kFetchTiles) fetch();
       if (round > 0 && !w.wait_warp(bar(empty + slot), (round - 1) & 1, code | (empty + slot))) {
         ok = false;

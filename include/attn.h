@@ -528,7 +528,9 @@ int attn_kv_append_debug_error(cudaStream_t stream, int* device_code);
  *   workspace         device, 16-byte aligned, attn_decode_kv8_workspace_bytes(B, Hq, Hkv, Nq, d,
  *                     num_splits) bytes, with the contract of attn_decode's (first 256 bytes zero
  *                     before the first call and after each; not shared by concurrent calls)
- *   opts              wait bound and CTA count as for attn_fwd_ex; may be NULL
+ *   opts              wait bound and CTA count as for attn_fwd_ex; inject_stall = n > 0: the loaders of a
+ *                     CTA stop before its n-th tile of 128 positions (test hook: waits run out and the call
+ *                     ends with ATTN_ERR_TIMEOUT pending, its outputs undefined); may be NULL
  *
  * Precision: the products take the codes exactly; a bf16 query row is split into two E4M3
  * terms (exact to 2^-17 of the row's largest element); scores, statistics and sums are fp32;
