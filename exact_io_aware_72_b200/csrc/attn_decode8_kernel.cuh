@@ -97,7 +97,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTop = 12.f;     // weights at the running maximum are 2^kTop
 constexpr float kGrow = 3.f;     // the running maximum moves when a row's grows by more
 constexpr float kNoMax = -3e38f; // running maximum of a row that has seen no key
-constexpr float kScaleMin = 9.094947017729282e-13f, kScaleMax = 1099511627776.f;  // 2^-40, 2^40
+// V scales c are taken within [2^-40, 2^60]; the append writes none below.  The sum of softmax weights
+// is formed from w / c, and w ends at fp32's 2^-126: with 100 powers of two between scales it
+// loses a key's softmax weight only below 2^-38 of that of the key that sets the maximum.
+constexpr float kScaleMin = 9.094947017729282e-13f, kScaleMax = 1152921504606846976.f;  // 2^-40, 2^60
 
 struct Dec8Params {
   CUtensorMap tm_k;        // [num_pages * Hkv][page_size][d] codes, box d x rows_per_load

@@ -454,7 +454,8 @@ int attn_decode_static(const void* q, const void* k_cache, const void* v_cache, 
  * NaN stays NaN), and a code is x / s rounded to nearest even. A block that held tokens of the
  * sequence before this call keeps its scale where its new tokens fit (amax <= 448 s);
  * otherwise it takes theirs, and its older codes are rounded again under it (which changes
- * their values only where they turn subnormal).
+ * their values only where they turn subnormal). (Values from 448 * 2^60 on, some 5e20, get scales that
+ * attn_decode_kv8 no longer takes.)
  *
  * Fields of the argument block (zero-initialise, then set what is needed):
  *   k, v          device, bf16, T rows of [Hkv, d]; k_stride, v_stride elements from row to row
@@ -517,7 +518,7 @@ int attn_kv_append_debug_error(cudaStream_t stream, int* device_code);
  *                     nothing of its table read, no error
  *   k_cache, v_cache  device, E4M3 codes, [num_pages, Hkv, page_size, d], contiguous, 16-byte aligned
  *   k_scale, v_scale  device, fp32, [num_pages, Hkv, page_size / scale_block], contiguous, 4-byte
- *                     aligned; finite. V scales are meant to lie in [2^-40, 2^40]: one outside is
+ *                     aligned; finite. V scales are meant to lie in [2^-40, 2^60]: one outside is
  *                     taken as the nearest bound
  *   scale_block       a power of two, at most page_size
  *   mask_kind         as attn_decode
