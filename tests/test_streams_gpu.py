@@ -74,3 +74,27 @@ def test_dropped_outputs_wait_for_the_current_stream(cuda_ok):
             others.append(torch.full_like(want, float("nan")))
     torch.cuda.synchronize()
     assert torch.equal(copy, want)
+
+
+@pytest.mark.parametrize("name", ["decode_kv8", "decode", "bwd", "kv_append"])
+def test_named_stream_inside_a_capture(cuda_ok, name):
+    """A call on a stream forked from the captured one: its buffers live in the graph's pool; one of its
+    results is dropped while the capture goes on."""
+    call = calls()[name]
+    want = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    main, side, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        call(stream=side)
+        got = call(stream=side)
+        main.wait_stream(side)
+        copies = [t.clone() for t in got]
+    for _ in range(3):
+        for t in (*got, *copies):
+            t.fill_(1.0)
+        graph.replay()
+        junk = [torch.full((1 << 20,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and all(torch.equal(a, b) for a, b in zip(copies, want))
+        del junk
