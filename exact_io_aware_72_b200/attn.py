@@ -497,7 +497,8 @@ def decode_kv8_workspace_bytes(B, Hq, Hkv, Nq, d, num_splits) -> int:
 
 def decode_kv8_workspace(B, Hq, Hkv, Nq, d, num_splits, device="cuda") -> torch.Tensor:
     """A zeroed workspace for ``decode_kv8`` steps of these sizes, to keep from step to step
-    (one for each stream or captured graph that may run at the same time)."""
+    (one for each stream or captured graph that may run at the same time).  The zeros are written
+    on the current stream, which the first step on another one has to wait for."""
     n = decode_kv8_workspace_bytes(B, Hq, Hkv, Nq, d, num_splits)
     if n < 1:
         raise ValueError("invalid decoding sizes")

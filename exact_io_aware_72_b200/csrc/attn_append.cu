@@ -25,7 +25,7 @@
 // groups head by head read the table anew for each, four lanes on a bank: 137 us instead of
 // 112 us for 16384 tokens of 64/8 heads.)  The heads are dealt over gridDim.y when there are
 // few units.  Measured: that chunk at 6000 GB/s, 92 % of a copy's; 8191 tokens of 32/8 heads
-// into E4M3 blocks of 16 in 44.6 us, 63 % (queries alone run at 80 %; a block's codes wait for
+// into E4M3 blocks of 16 in 44.2 us, 63 % (queries alone run at 80 %; a block's codes wait for
 // the maximum of 16 rows, a barrier a head).
 #include "attn.h"
 

@@ -57,9 +57,10 @@
 // 10 us an item.
 //
 // Measured, with the bytes of the visible codes and scales over 6544 GB/s (a copy) as 100 %: one
-// sequence of 131072 positions, 64/8 heads, 49.4 us (83 %: the start and the end of the one wave
-// of items, the merge and the launches, 8 us, are not overlapped); 16 of 8k-32k with 32 heads 416 us (99 %); 32 windows of 4096 with
-// 4 sinks 52 us (79 %); 8 of 16k-32k with 32 rows (four new tokens, groups of 8) 114 us (54 %: the
+// sequence of 131072 positions, 64/8 heads, 49.5 us (83 %: the start and the end of the one wave
+// of items, the merge and the launches, 8 us, are not overlapped); 16 of 8k-32k with 32 heads 415 to
+// 438 us (99 to 94 %); 32 windows of 4096 with
+// 4 sinks 52 us (79 %); 8 of 16k-32k with 32 rows (four new tokens, groups of 8) 116 us (53 %: the
 // softmax warps' 3300 cycles a tile, two tiles at a time on an SM, against the 1400 in
 // which HBM delivers one).
 #pragma once
