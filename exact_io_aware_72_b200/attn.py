@@ -156,22 +156,46 @@ def _stream_handle(stream: Optional[torch.cuda.Stream], index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
+class _Current:
+    """``stream`` current on its device (torch.cuda.stream without the Stream objects, 9 us each)."""
+    __slots__ = ("stream", "before")
+
+    def __init__(self, stream: torch.cuda.Stream):
+        self.stream = stream
+
+    def __enter__(self):
+        s = self.stream
+        self.before = torch._C._cuda_getCurrentStream(s.device_index)
+        with _on_device(s.device_index):
+            torch._C._cuda_setStream(stream_id=s.stream_id, device_index=s.device_index, device_type=s.device_type)
+
+    def __exit__(self, *exc):
+        stream_id, index, kind = self.before
+        with _on_device(index):
+            torch._C._cuda_setStream(stream_id=stream_id, device_index=index, device_type=kind)
+
+
+def _is_other(stream: Optional[torch.cuda.Stream]) -> bool:
+    """Does the call name a stream that is not its device's current one?"""
+    return stream is not None and torch._C._cuda_getCurrentRawStream(stream.device_index) != stream.cuda_stream
+
+
 def _on_stream(stream: Optional[torch.cuda.Stream]):
     """Context in which a call allocates (and fills) what its caller did not bring: ``stream`` current,
     so that a block's earlier use, its fill, the kernels and its next use follow one another there.
     Blocks of the current stream would be taken while that stream's earlier work still uses them,
     filled without an order, and handed on while ``stream`` still runs."""
-    return _NO_SWITCH if stream is None else torch.cuda.stream(stream)
+    return _Current(stream) if _is_other(stream) else _NO_SWITCH
 
 
 def _output(like: torch.Tensor, stream: Optional[torch.cuda.Stream], shape=None, dtype=None) -> torch.Tensor:
     """A new output of a call on ``stream``, by default like ``like``.  Its block, once the caller drops
     it, also waits for what the caller's current stream has been given by then."""
-    if stream is None:
+    if not _is_other(stream):
         return torch.empty_like(like, dtype=dtype) if shape is None else like.new_empty(shape, dtype=dtype)
-    with torch.cuda.stream(stream):
+    with _Current(stream):
         t = torch.empty_like(like, dtype=dtype) if shape is None else like.new_empty(shape, dtype=dtype)
-    t.record_stream(torch.cuda.current_stream(like.device))
+    t.record_stream(torch.cuda.current_stream(stream.device_index))
     return t
 
 
@@ -623,7 +647,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     rotation on, by the cache's positions or ``positions`` (int32 [T]).  With ``q``
     [T, Hq, d] its rotated rows are returned: [B, Hq, T / B, d] as ``decode`` takes them, or
     [T, Hq, d] with ``cu_tokens``.  Without ``cu_tokens`` seq_lens[b] = 0 marks an idle slot, as in
-    ``decode_kv8``: nothing of it is read or cached, its queries are zeros.  One launch on ``stream`` (default: the current stream).
+    ``decode_kv8``: nothing of it is read or cached, its queries are zeros.  One launch on ``stream``
+    (default: the current stream).
     """
     lib = load_library()
     k_stride = _rows(k, "k", None, None, None)

@@ -41,7 +41,7 @@ class Library:
         return (lambda *a: 4096) if "workspace_bytes" in name else (lambda *a: 1 if "num_splits" in name else 0)
 
 
-SIDE = types.SimpleNamespace(name="side", cuda_stream=1234, synchronize=lambda: None)
+SIDE = types.SimpleNamespace(name="side", cuda_stream=1234, device_index=0, synchronize=lambda: None)
 
 
 @pytest.fixture
@@ -53,7 +53,8 @@ def streams(monkeypatch):
     monkeypatch.setattr(A, "_rows", lambda t, *a: t.stride(0))
     monkeypatch.setattr(A, "_on_device", lambda index: contextlib.nullcontext())
     monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
-    monkeypatch.setattr(torch.cuda, "stream", mode.stream)
+    monkeypatch.setattr(A, "_is_other", lambda s: s is not None and s.name != mode.current)
+    monkeypatch.setattr(A, "_Current", mode.stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(name=mode.current))
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: mode.recorded.append((t, s.name)))
     monkeypatch.setattr(torch.Tensor, "is_cuda", True)
@@ -97,12 +98,13 @@ def test_a_named_stream_owns_what_its_call_allocates(streams, call):
     assert all(any(same(t, g) and s == "current" for t, s in streams.recorded) for g in got)
 
 
+@pytest.mark.parametrize("name", [None, "current"])
 @pytest.mark.parametrize("call", sorted(inputs()))
-def test_without_a_stream_nothing_is_switched(streams, call, monkeypatch):
+def test_on_the_current_stream_nothing_is_switched(streams, call, name, monkeypatch):
     monkeypatch.setattr(A, "_stream_handle", lambda stream, index: 0)
     fn = inputs()[call]
     with streams:
-        fn()
+        fn(stream=name and types.SimpleNamespace(name=name, cuda_stream=0))
     assert streams.made and all(s == "current" for _, s in streams.made) and not streams.recorded
 
 
