@@ -566,8 +566,8 @@ def decode_kv8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_
         scale = 1.0 / math.sqrt(d)
     max_pages = block_table.shape[1]
     if num_splits is None:
-        num_splits = decode_kv8_num_splits(B, Hq, Hkv, Nq, max_pages * page_size if max_seq_len is None else max_seq_len,
-                                           mask, window, sinks)
+        longest = max_pages * page_size if max_seq_len is None else int(max_seq_len)
+        num_splits = decode_kv8_num_splits(B, Hq, Hkv, Nq, max(longest, Nq), mask, window, sinks)  # (all slots may be idle)
     if out is None:
         out = _output(q, stream)
     if lse is None:

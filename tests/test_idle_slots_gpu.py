@@ -123,3 +123,20 @@ def test_captured_padded_generation(cuda_ok, splits):
         assert torch.equal(out[live], want[0]) and torch.equal(lse[live], want[1])
         assert not out[idle].any() and torch.isneginf(lse[idle]).all()
         assert all(torch.equal(raw(s[c]), raw(t[c])) for c in ("k_cache", "v_cache", "k_scale", "v_scale"))
+
+
+def test_the_longest_length_may_be_an_idle_batchs(cuda_ok):
+    """max_seq_len only picks the splits: a batch that has fallen idle passes 0, or what it has."""
+    import exact_io_aware_72_b200 as attn
+    s = state(3, 1, 128, 16, [0, 0, 0], 6)
+    q = append(s)
+    for longest in (0, 1, None):
+        out, lse = attn.decode_kv8(q, s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"], s["block_table"],
+                                   s["seq_lens"], max_seq_len=longest)
+        assert not out.any() and torch.isneginf(lse).all()
+    # more new tokens a slot than its table has positions
+    q = torch.randn(2, HQ, 80, 128).bfloat16().cuda()
+    out, lse = attn.decode_kv8(q, s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"], s["block_table"][:2, :1].contiguous(),
+                               s["seq_lens"][:2].contiguous(), max_seq_len=0)
+    torch.cuda.synchronize()
+    assert not out.any() and attn.decode_kv8_debug_error() == (0, 0)
