@@ -131,7 +131,18 @@ struct SmemLayout {
   static constexpr int kChunkElems = 128 / EB;                   // elements in a 128-byte chunk row
   static constexpr uint32_t kChunkBytes = kBlockM * 128;         // 128 rows x 128 B
   static constexpr uint32_t kTileBytes = kChunks * kChunkBytes;  // one Q, K or V tile
-  static constexpr int kStages = (kChunks == 2) ? 5 : 8;         // K/V ring slots
+  static constexpr int kStages = (kChunks == 2) ? 5 : 8;         // K/V slots
+  // K and V take turns on slots of their own.  A wait for a slot's phase also passes two phases early,
+  // so whoever waits for a load must have seen the slot's load before it: warp 11 waits for V
+  // alone.  (On one ring of five slots V_v followed K_{v-2}.  With V_{v-1} landed and that K tile still
+  // on its way from HBM, warp 11 took it for V_v and converted under its copy: one call in a
+  // thousand gave an item of 256 wrong rows.)
+  static constexpr int kKSlots = kStages / 2, kVSlots = kStages - kKSlots;
+  // Slot (of the kStages) and phase parity of the K and V tiles of step n.
+  static __device__ __forceinline__ uint32_t k_slot(uint32_t n) { return n % kKSlots; }
+  static __device__ __forceinline__ uint32_t k_parity(uint32_t n) { return (n / kKSlots) & 1; }
+  static __device__ __forceinline__ uint32_t v_slot(uint32_t n) { return kKSlots + n % kVSlots; }
+  static __device__ __forceinline__ uint32_t v_parity(uint32_t n) { return (n / kVSlots) & 1; }
   static constexpr uint32_t kQOff = 0;
   static constexpr uint32_t kKVOff = 2 * kTileBytes;
   static constexpr uint32_t kBarOff = kKVOff + kStages * kTileBytes;
@@ -358,7 +369,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // arrive on kVConv[v % kConvRing] for K/V step v, and the P V of step v waits
 // there.  A barrier of the ring is reused four steps later; by then both MMA
 // warps have passed its previous phase, because V_{v+4} cannot land before the
-// P V of step v has released ring space.
+// P V of step v has released its slot (there are at most four).
 template <int D, int EB>
 struct VConvSplit {
   static constexpr int kUnits = static_cast<int>(SmemLayout<D, EB>::kTileBytes / 16);  // 16-byte units
@@ -397,14 +408,14 @@ template <int D, int EB, bool SINK>
 __device__ __forceinline__ void vconv_role(const FwdParams& p, uint32_t sbase, const Waiter& w, int lane) {
   using L = SmemLayout<D, EB>;
   auto bar = [&](int i) { return sbase + L::kBarOff + 8u * i; };
-  uint32_t v = 0;  // K/V steps so far; V of step v is load 2v + 1
+  uint32_t v = 0;  // K/V steps so far
   Schedule sched(p, blockIdx.x, gridDim.x);
   int hu, r;
   while (sched.next(hu, r)) {
     const WorkItem it = decode_item<SINK>(p, hu, r);
     for (int u = it.first_u<SINK>(); u <= it.hi_u; ++u, ++v) {
-      const uint32_t vn = 2 * v + 1, slot = vn % L::kStages;
-      const bool got = w.wait(bar(L::kKVFull + slot), (vn / L::kStages) & 1, (kRoleVConv << 8) | (L::kKVFull + slot));
+      const uint32_t slot = L::v_slot(v);
+      const bool got = w.wait(bar(L::kKVFull + slot), L::v_parity(v), (kRoleVConv << 8) | (L::kKVFull + slot));
       if (!__all_sync(0xffffffffu, got)) return;
       const uint32_t mag = convert_v_units(sbase + L::kKVOff + slot * L::kTileBytes, 0, VConvSplit<D, EB>::kWarp11, lane);
       finish_v_part(bar(L::kVConv + (v % kConvRing)), mag, w.err, lane);
@@ -447,7 +458,7 @@ __device__ __forceinline__ void producer_role(const FwdParams& p, uint32_t sbase
   tma_prefetch_map(&p.tm_k);
   tma_prefetch_map(&p.tm_v);
 
-  uint32_t kv_n = 0;  // K/V loads issued so far
+  uint32_t k_n = 0, v_n = 0;  // K and V loads issued so far
   uint32_t q_issued = 0;
   int items = 0;
   bool ok = !p.inject_stall;
@@ -482,12 +493,22 @@ __device__ __forceinline__ void producer_role(const FwdParams& p, uint32_t sbase
     for (int u = it.first_u<SINK>(); u <= it.hi_u && ok; ++u) {
       const int j = it.tile<SINK>(u);
       if (u == pf_step) prefetch_next_item<D, EB, SINK>(p, sched);
+      // V first, whose slot is free earlier (behind the P V of three steps before, K's behind the S
+      // after it) and whose conversion comes before the step's S; but K first where an item begins,
+      // and with sinks throughout.  (Measured, K first throughout / in the first step / in four.
+      // d = 128: B = 2, N = 8192, 32 heads 1108 / 1079 / 1073 us, window 1024 880 / 894 / 882, with 16
+      // sinks 875 / 928 / 965; window 4096 and 4 sinks, N = 131072, 9700 throughout, 10120 in four.
+      // d = 64: the same heads 949 / 908 / 908, window 1024 with 16 sinks 727 / 700 / 710.)
+      const bool first = u == it.first_u<SINK>();
+      const bool k_first = D == 64 ? first : (SINK || u < it.first_u<SINK>() + 4);
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t slot = kv_n % L::kStages;
-        if (kv_n >= (uint32_t)L::kStages &&
-            !w.wait(bar(L::kKVEmpty + slot), ((kv_n / L::kStages) - 1) & 1,
-                    (kRoleProducer << 8) | (L::kKVEmpty + slot))) {
+      for (int i = 0; i < 2; ++i) {
+        const bool kv = k_first ? i == 1 : i == 0;
+        const uint32_t slot = kv ? L::v_slot(v_n) : L::k_slot(k_n);
+        const bool used = kv ? v_n >= (uint32_t)L::kVSlots : k_n >= (uint32_t)L::kKSlots;
+        // (the phase before the one that this load completes)
+        if (used && !w.wait(bar(L::kKVEmpty + slot), (kv ? L::v_parity(v_n) : L::k_parity(k_n)) ^ 1,
+                            (kRoleProducer << 8) | (L::kKVEmpty + slot))) {
           ok = false;
           break;
         }
@@ -497,8 +518,8 @@ __device__ __forceinline__ void producer_role(const FwdParams& p, uint32_t sbase
         for (int c = 0; c < L::kChunks; ++c)
           tma_load_3d(sbase + L::kKVOff + slot * L::kTileBytes + c * L::kChunkBytes, map,
                       bar(L::kKVFull + slot), c * L::kChunkElems, j * kBlockN, it.b * p.Hkv + it.hkv, pol_kv);
-        ++kv_n;
-        if (u == it.first_u<SINK>() && kv == 1 && !load_q()) {
+        ++(kv ? v_n : k_n);
+        if (first && kv && !load_q()) {
           ok = false;
           break;
         }
@@ -507,11 +528,14 @@ __device__ __forceinline__ void producer_role(const FwdParams& p, uint32_t sbase
     ++items;
   }
   // Drain: every copy this thread started must land before the CTA exits.
-  for (uint32_t s = 0; s < (uint32_t)L::kStages; ++s) {
-    if (kv_n > s) {
-      const uint32_t last = s + ((kv_n - 1 - s) / L::kStages) * L::kStages;  // last load into slot s
-      w.drain(bar(L::kKVFull + s), (last / L::kStages) & 1, (kRoleProducer << 8) | (L::kKVFull + s));
-    }
+  // (a slot is loaded again only after its load landed, so the last one of each is waited for)
+  for (uint32_t back = 1; back <= (uint32_t)L::kKSlots && back <= k_n; ++back) {
+    const uint32_t slot = L::k_slot(k_n - back);
+    w.drain(bar(L::kKVFull + slot), L::k_parity(k_n - back), (kRoleProducer << 8) | (L::kKVFull + slot));
+  }
+  for (uint32_t back = 1; back <= (uint32_t)L::kVSlots && back <= v_n; ++back) {
+    const uint32_t slot = L::v_slot(v_n - back);
+    w.drain(bar(L::kKVFull + slot), L::v_parity(v_n - back), (kRoleProducer << 8) | (L::kKVFull + slot));
   }
   if (q_issued > 0) w.drain(bar(L::kQFull), (q_issued - 1) & 1, (kRoleProducer << 8) | L::kQFull);
 }
@@ -552,10 +576,10 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
     return __all_sync(0xffffffffu, got);
   };
 
-  // This warp's quarter of the V tile of K/V step v (load 2v + 1) to fp16.
+  // This warp's quarter of the V tile of K/V step v to fp16.
   auto convert_quarter = [&](uint32_t v) -> bool {
-    const uint32_t vn = 2 * v + 1, vslot = vn % L::kStages;
-    if (!wait_all(bar(L::kKVFull + vslot), (vn / L::kStages) & 1, code | (L::kKVFull + vslot))) return false;
+    const uint32_t vslot = L::v_slot(v);
+    if (!wait_all(bar(L::kKVFull + vslot), L::v_parity(v), code | (L::kKVFull + vslot))) return false;
     const uint32_t mag = convert_v_units(sbase + L::kKVOff + vslot * L::kTileBytes,
                                          VConvSplit<D, EB>::kWarp11 + t * VConvSplit<D, EB>::kMma,
                                          VConvSplit<D, EB>::kMma, threadIdx.x & 31);
@@ -563,7 +587,7 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
     return true;
   };
 
-  uint32_t kv_n = 0;
+  uint32_t n = 0;  // K/V steps so far
   uint32_t p_cnt = 0;
   int items = 0;
   bool ok = true;
@@ -590,26 +614,25 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
     bool pend = false;
     bool first_pv = true;
 
-    // The V tile with load index vn has landed (a tile this warp does not
+    // The V tile of step v has landed (a tile this warp does not
     // read must still be seen before this warp releases it).
-    auto wait_v_landed = [&](uint32_t vn) -> bool {
-      const uint32_t vslot = vn % L::kStages;
-      return wait_all(bar(L::kKVFull + vslot), (vn / L::kStages) & 1, code | (L::kKVFull + vslot));
+    auto wait_v_landed = [&](uint32_t v) -> bool {
+      const uint32_t vslot = L::v_slot(v);
+      return wait_all(bar(L::kKVFull + vslot), L::v_parity(v), code | (L::kKVFull + vslot));
     };
-    // O_t += P_t V for the V tile with load index vn.
-    auto issue_pv = [&](uint32_t vn) -> bool {
+    // O_t += P_t V for the V tile of step v.
+    auto issue_pv = [&](uint32_t v) -> bool {
       if (first_pv && items > 0 && !wait_all(bar(L::kOFree + t), (items - 1) & 1, code | (L::kOFree + t)))
         return false;
       if (!wait_all(bar(L::kPFull + t), p_cnt & 1, code | (L::kPFull + t))) return false;
       ++p_cnt;
-      const uint32_t vslot = vn % L::kStages;
+      const uint32_t vslot = L::v_slot(v);
       // With fp16 P the conversion barrier below implies the tile landed (its
       // converters waited for that), and the product reads only bytes they rewrote.
-      if (!kConvV && !wait_all(bar(L::kKVFull + vslot), (vn / L::kStages) & 1, code | (L::kKVFull + vslot)))
+      if (!kConvV && !wait_all(bar(L::kKVFull + vslot), L::v_parity(v), code | (L::kKVFull + vslot)))
         return false;
       if constexpr (kConvV) {
-        // Warp 11 and both MMA warps have converted this V tile (K/V step vn / 2) to fp16.
-        const uint32_t v = vn >> 1;
+        // Warp 11 and both MMA warps have converted this V tile to fp16.
         if (!wait_all(bar(L::kVConv + (v % kConvRing)), (v / kConvRing) & 1, code | (L::kVConv + (v % kConvRing))))
           return false;
       }
@@ -632,19 +655,19 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
 
     for (int u = it.first_u<SINK>(); u <= it.hi_u; ++u) {
       const int j = it.tile<SINK>(u);
-      const uint32_t kslot = kv_n % L::kStages;
+      const uint32_t kslot = L::k_slot(n);
       // K_j is normally resident long before P_t(j-1) is ready; confirming it
       // first lets P V and the next S issue back to back once P arrives.
-      if (!wait_all(bar(L::kKVFull + kslot), (kv_n / L::kStages) & 1, code | (L::kKVFull + kslot))) {
+      if (!wait_all(bar(L::kKVFull + kslot), L::k_parity(n), code | (L::kKVFull + kslot))) {
         ok = false;
         break;
       }
       if (pend) {
-        if (!issue_pv(kv_n - 1)) {
+        if (!issue_pv(n - 1)) {
           ok = false;
           break;
         }
-      } else if (u > it.first_u<SINK>() && !wait_v_landed(kv_n - 1)) {
+      } else if (u > it.first_u<SINK>() && !wait_v_landed(n - 1)) {
         ok = false;
         break;
       }
@@ -670,21 +693,21 @@ __device__ __forceinline__ void mma_role(const FwdParams& p, uint32_t sbase, uin
       // arrival for a load can only come after the load was issued, i.e.
       // after the slot's previous phase completed: no warp ever arrives twice
       // in one phase, even when its own tile is idle and it runs ahead.
-      if (u > it.first_u<SINK>()) tc_commit_elect(bar(L::kKVEmpty + (kv_n - 1) % L::kStages));  // V_{j-1} read
+      if (u > it.first_u<SINK>()) tc_commit_elect(bar(L::kKVEmpty + L::v_slot(n - 1)));  // V_{j-1} read
       tc_commit_elect(bar(L::kKVEmpty + kslot));                                   // K_j read
       if (u == it.hi_u) tc_commit_elect(bar(L::kQEmpty));                          // Q read
       if constexpr (kConvV) {
         // This warp's quarter of the next step's V (its P V comes a step later).
-        if ((u < it.hi_u || more_items) && !convert_quarter((kv_n >> 1) + 1)) {
+        if ((u < it.hi_u || more_items) && !convert_quarter(n + 1)) {
           ok = false;
           break;
         }
       }
-      kv_n += 2;
+      ++n;
     }
     if (!ok) break;
-    if (pend ? !issue_pv(kv_n - 1) : !wait_v_landed(kv_n - 1)) break;
-    tc_commit_elect(bar(L::kKVEmpty + (kv_n - 1) % L::kStages));  // V_hi read
+    if (pend ? !issue_pv(n - 1) : !wait_v_landed(n - 1)) break;
+    tc_commit_elect(bar(L::kKVEmpty + L::v_slot(n - 1)));  // V_hi read
     if (first_pv && items > 0 && !wait_all(bar(L::kOFree + t), (items - 1) & 1, code | (L::kOFree + t))) break;
     tc_commit_elect(bar(L::kODone + t));
     ++items;
