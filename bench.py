@@ -61,9 +61,9 @@ KERNEL_SOURCES = ["exact_io_aware_72_b200/csrc/attn_fwd.cu", "exact_io_aware_72_
 # N = 32768 case (1, 32, 32, 32768, 128) times 4: DRAM bytes grow linearly in N.
 # The FP8 long figure is a capture of the full launch (E4M3 q, k, v: 1.2 GiB).
 NCU_TRAFFIC = {
-    ("dense", "5524022e3804babe"): 408917248 + 111116800,
-    ("long", "5524022e3804babe"): 4 * (918392832 + 252631552),
-    ("long_fp8", "5524022e3804babe"): 2164523776 + 1076452096,
+    ("dense", "2d6090b5af12600b"): 408875776 + 110926336,
+    ("long", "2d6090b5af12600b"): 4 * (909379072 + 252205568),
+    ("long_fp8", "2d6090b5af12600b"): 2132362496 + 1075280896,
 }
 
 
