@@ -61,9 +61,9 @@ KERNEL_SOURCES = ["exact_io_aware_72_b200/csrc/attn_fwd.cu", "exact_io_aware_72_
 # N = 32768 case (1, 32, 32, 32768, 128) times 4: DRAM bytes grow linearly in N.
 # The FP8 long figure is a capture of the full launch (E4M3 q, k, v: 1.2 GiB).
 NCU_TRAFFIC = {
-    ("dense", "2d6090b5af12600b"): 408875776 + 110926336,
-    ("long", "2d6090b5af12600b"): 4 * (909379072 + 252205568),
-    ("long_fp8", "2d6090b5af12600b"): 2132362496 + 1075280896,
+    ("dense", "587ef0136dcb0561"): 408509952 + 111154176,
+    ("long", "587ef0136dcb0561"): 4 * (907349248 + 253553152),
+    ("long_fp8", "587ef0136dcb0561"): 2133067520 + 1075190528,
 }
 
 
